@@ -320,6 +320,74 @@ int sa_prune_compact(const sa_geom* g, const void* k_cache, const void* v_cache,
                      int32_t* pos_map, int32_t* logical_len, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * (6) Filling the cache and attending from new tokens: the step before a decode (a prompt,
+ * a chunk of one, drafted tokens to check, or the decode's own new token).  The pages name
+ * prefill next to decode (SC task table and Tri-shape section) and give no formula; both
+ * calls are the plain definitions below.
+ *
+ * A call takes a ragged batch of n_tokens rows: rows [cu_new[b], cu_new[b+1]) are the new
+ * tokens of sequence b (n_b of them, possibly none), in order.  seq_lens[b] is the length
+ * AFTER the append, as every other call of this library expects it, so new token i of
+ * sequence b lives in slot s = seq_lens[b] - n_b + i.  Rows at or behind cu_new[B] belong to
+ * no sequence: nothing is read for them and their outputs keep their contents.
+ * n_tokens = 0 is legal and launches nothing.  A sequence with cu_new[b] < 0,
+ * cu_new[b] > cu_new[b+1], cu_new[b+1] > n_tokens, seq_lens[b] < n_b or seq_lens[b] >
+ * max_pages * P is left out and reported as SA_ERR_DEVICE_CHECK.
+ *
+ * sa_append_kv.  Position of new token i: pos = logical_lens[b] - n_b + i (logical_lens
+ * nullable: seq_lens), so that a session whose cache was pruned goes on counting from its
+ * position marker (sa_prune_compact's logical_len plus the tokens since).  Channels
+ * [rot_start, rot_start + rot_dim) of every query and key row are rotated by the angles
+ * pos * inv_freq[j], j < rot_dim / 2: channel pairs (j, j + rot_dim/2), or (2j, 2j+1) when
+ * `interleaved`:  (x, y) -> (x cos - y sin, y cos + x sin).  The angle is formed and reduced
+ * in fp64, the rotation is fp32, rounded once to bf16.  rot_dim = 0 (inv_freq nullable):
+ * nothing is rotated.
+ *   k [n_tokens][Hkv][Dk], v [n_tokens][Hkv][Dv] (ignored when v_aliases_k), q
+ *   [n_tokens][Hq][Dk] (nullable): bf16, each row of heads dense, *_stride elements from one
+ *   token to the next (>= the row, a multiple of 8), so slices of one fused projection
+ *   output need no copy.  q_out [n_tokens][Hq][Dk] dense; q_out == q is allowed with
+ *   q_stride = Hq * Dk, any other overlap between inputs and outputs is not.
+ *   K rows (rotated) and V rows go to their slots of the pages page_table names.
+ *   summ / summ8 (nullable; at most one non-null): the bf16 summaries or fp8 records of
+ *   every page that received a token are recomputed over all its valid tokens, exactly as
+ *   sa_page_summaries / sa_page_summaries_fp8 would (summ8: grouped-query geometry).
+ * A page that receives a token must belong to one sequence of the call only (a shared
+ * partial page has to be copied first).  A page-table entry outside [0, n_pool) of a page
+ * that would receive tokens is reported as SA_ERR_DEVICE_CHECK and the page's tokens are
+ * left out, their q_out rows included.
+ * rot_dim: a multiple of 16, rot_dim <= 128; rot_start a multiple of 8, rot_start + rot_dim
+ * <= Dk.  inv_freq [rot_dim/2] fp32 on the device.  ws: any workspace of >= 256 bytes (only
+ * the status word is used).
+ * ------------------------------------------------------------------------------ */
+int sa_append_kv(const sa_geom* g, const void* q, int64_t q_stride, const void* k,
+                 int64_t k_stride, const void* v, int64_t v_stride, int n_tokens,
+                 const int32_t* cu_new, const int32_t* page_table, const int32_t* seq_lens,
+                 const int32_t* logical_lens, const float* inv_freq, int rot_start, int rot_dim,
+                 int interleaved, void* q_out, void* k_cache, void* v_cache, void* summ,
+                 void* summ8, void* ws, size_t ws_bytes, void* stream);
+
+/* sa_attend_chunk: exact softmax attention of the new tokens over their sequences' caches
+ * (which already hold them, see sa_append_kv).  A query in slot s sees the tokens t <= s
+ * with, when window > 0, also t > s - window or t < sink (sink tokens + local window, SC
+ * Tri-shape section; any token counts >= 0; sink is ignored when window = 0):
+ *   x_t = scale * q . k_t;  out = sum_t softmax(x)_t v_t;  lse = log sum_t exp(x_t).
+ *   q [n_tokens][Hq][Dk] bf16, out [n_tokens][Hq][Dv] bf16 (the operand of the output
+ *   projection; half the bytes of the decode calls' fp32), lse [n_tokens][Hq] fp32.
+ * scale must be positive and finite.  Scores, softmax statistics and sums are fp32; the
+ * probabilities are rounded to bf16 (relative to a running maximum) for the product with V,
+ * and out once at the end.  Storage behind seq_lens[b] is never used.  Results do not depend
+ * on what else runs and repeat bit for bit.  A page-table entry outside [0, n_pool) of a
+ * page holding visible tokens is reported as SA_ERR_DEVICE_CHECK; the rows that see such a
+ * page are then unspecified.  One new token per sequence (n_b = 1) is the dense decode.
+ * sa_chunk_workspace_size: bytes needed for up to n_tokens rows (0 on invalid arguments);
+ * any decode workspace of at least that size serves too. */
+size_t sa_chunk_workspace_size(const sa_geom* g, int n_tokens);
+int sa_attend_chunk(const sa_geom* g, const void* q, int n_tokens, const int32_t* cu_new,
+                    const void* k_cache, const void* v_cache, const int32_t* page_table,
+                    const int32_t* seq_lens, int sink, int window, float scale, void* out,
+                    float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

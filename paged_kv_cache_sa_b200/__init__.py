@@ -16,6 +16,10 @@ Functions (all asynchronous on ``torch.cuda.current_stream()``):
   attend_selected(geom, q, k_cache, v_cache, page_table, seq_lens, sel, sel_count,
                   scale, out, lse, ws)
   prune_compact(geom, k_cache, v_cache, page_table, seq_lens, keep, free_pages, ...)
+  append_kv(geom, k, v, cu_new, page_table, seq_lens, k_cache, v_cache, ws, q, inv_freq,
+            logical_lens, summ, ...)
+  attend_chunk(geom, q, cu_new, k_cache, v_cache, page_table, seq_lens, scale, ws, sink,
+               window, out, lse)
 
 ``Workspace`` owns one zero-initialised device buffer sized for a geometry.
 """
@@ -34,6 +38,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libsa.so")
 
 SA_OK = 0
 SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE = -1, -2, -3
+SA_ERR_CUDA, SA_ERR_DEVICE_CHECK, SA_ERR_TIMEOUT, SA_ERR_NO_SPACE = -4, -5, -6, -7
 STATUS = {0: "SA_OK", -1: "SA_ERR_INVALID_ARG", -2: "SA_ERR_UNSUPPORTED", -3: "SA_ERR_WORKSPACE",
           -4: "SA_ERR_CUDA", -5: "SA_ERR_DEVICE_CHECK", -6: "SA_ERR_TIMEOUT",
           -7: "SA_ERR_NO_SPACE"}
@@ -44,7 +49,8 @@ EXPORTS = ["sa_status_string", "sa_version", "sa_decode_workspace_size", "sa_pru
            "sa_page_scores", "sa_select_pages", "sa_sparse_decode", "sa_attend_selected",
            "sa_prune_compact", "sa_sparse_decode_noalloc", "sa_summary_fp8_record_bytes",
            "sa_page_summaries_fp8", "sa_update_summaries_fp8", "sa_page_scores_fp8",
-           "sa_sparse_decode_fp8", "sa_sparse_decode_fused"]
+           "sa_sparse_decode_fp8", "sa_sparse_decode_fused", "sa_append_kv",
+           "sa_chunk_workspace_size", "sa_attend_chunk"]
 
 
 class SaError(RuntimeError):
@@ -112,6 +118,11 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
                                   vp, vp, vp, vp, vp, sz, vp], i32),
         "sa_attend_selected": ([G, vp, vp, vp, vp, vp, vp, vp, vp, i32, ctypes.c_float, vp, vp,
                                 vp, sz, vp], i32),
+        "sa_append_kv": ([G, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, i32,
+                          vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "sa_chunk_workspace_size": ([G, i32], sz),
+        "sa_attend_chunk": ([G, vp, i32, vp, vp, vp, vp, vp, i32, i32, ctypes.c_float, vp, vp,
+                             vp, sz, vp], i32),
         "sa_prune_compact": ([G, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                               vp], i32),
     }
@@ -150,6 +161,11 @@ def decode_workspace_size(geom: Geometry, budget: int) -> int:
     return int(lib.sa_decode_workspace_size(ctypes.byref(g), int(budget)))
 
 
+def chunk_workspace_size(geom: Geometry, n_tokens: int) -> int:
+    g = geom.c()
+    return int(lib.sa_chunk_workspace_size(ctypes.byref(g), int(n_tokens)))
+
+
 def prune_workspace_size(geom: Geometry) -> int:
     g = geom.c()
     return int(lib.sa_prune_workspace_size(ctypes.byref(g)))
@@ -169,6 +185,11 @@ class Workspace:
     @classmethod
     def for_decode(cls, geom: Geometry, budget: int, **kw) -> "Workspace":
         return cls(decode_workspace_size(geom, budget), **kw)
+
+    @classmethod
+    def for_chunk(cls, geom: Geometry, n_tokens: int, **kw) -> "Workspace":
+        """For append_kv and attend_chunk calls of up to ``n_tokens`` rows."""
+        return cls(chunk_workspace_size(geom, n_tokens), **kw)
 
     @classmethod
     def for_prune(cls, geom: Geometry, **kw) -> "Workspace":
@@ -383,3 +404,113 @@ def prune_compact(geom: Geometry, k_cache, v_cache, page_table, seq_lens, keep, 
                                 _ptr(logical_len), _ptr(ws.buf), ws.nbytes, _stream(stream)),
            "sa_prune_compact")
     return new_page_table, new_seq_lens, pos_map, logical_len
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 values or their bit patterns
+
+
+def _need(t, name, shape, dtypes, device):
+    """A dense tensor of this shape and type on ``device`` (ValueError otherwise): the
+    library sees plain pointers and could not tell."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != device:
+        raise ValueError("%s: need shape %s of %s on %s, got %s of %s on %s" % (
+            name, list(shape), dtypes[0], device, list(t.shape), t.dtype, t.device))
+    return _ptr(t)
+
+
+def _rows(t, name, heads, width, n, device):
+    """(pointer, elements per token) of [n, heads, width] rows; only tokens may be strided."""
+    if t.shape != (n, heads, width) or t.dtype not in _BF16 or t.device != device:
+        raise ValueError("%s: need shape %s of torch.bfloat16 on %s, got %s of %s on %s" % (
+            name, [n, heads, width], device, list(t.shape), t.dtype, t.device))
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if n == 0:
+        return ctypes.c_void_p(t.data_ptr() or 16), heads * width
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != width):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return ctypes.c_void_p(t.data_ptr()), s0 if n > 1 else max(s0, heads * width) & ~7
+
+
+def _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, device):
+    i32, pool = (torch.int32,), (geom.n_pool, geom.Hkv, geom.P)
+    ptrs = [_need(cu_new, "cu_new", (geom.B + 1,), i32, device),
+            _need(page_table, "page_table", (geom.B, geom.max_pages), i32, device),
+            _need(seq_lens, "seq_lens", (geom.B,), i32, device),
+            _need(k_cache, "k_cache", pool + (geom.Dk,), _BF16, device)]
+    v = None
+    if not geom.v_aliases_k:
+        if v_cache is None:
+            raise ValueError("v_cache is needed (the geometry's V does not alias K)")
+        v = _need(v_cache, "v_cache", pool + (geom.Dv,), _BF16, device)
+    return ptrs + [v]
+
+
+def append_kv(geom: Geometry, k, v, cu_new, page_table, seq_lens, k_cache, v_cache,
+              ws: Workspace, q=None, q_out=None, inv_freq=None, rot_start: int = 0,
+              interleaved: bool = False, logical_lens=None, summ=None, summ8=None, stream=None):
+    """Write the new tokens' K and V rows to the paged cache, rotating keys (and queries) by
+    their positions, and refresh the summaries of the pages written (``summ``: bf16 rows,
+    ``summ8``: fp8 records).
+
+    Rows ``cu_new[b]:cu_new[b+1]`` are sequence b's new tokens; ``seq_lens`` counts them
+    already.  ``k`` [n, Hkv, Dk], ``v`` [n, Hkv, Dv], ``q`` [n, Hq, Dk] may be slices of one
+    projection output (only the token stride may differ from dense).  ``inv_freq`` [rot/2]
+    fp32 gives the rotated width; None rotates nothing.  Returns ``q_out`` (allocated when
+    ``q`` is given without it; rows of no sequence are then undefined), else None."""
+    dev, n = k_cache.device, k.shape[0]
+    cu, pt, sl, kc, vc = _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, dev)
+    kp, ks = _rows(k, "k", geom.Hkv, geom.Dk, n, dev)
+    vp, vs, qp, qs = None, 0, None, 0
+    if not geom.v_aliases_k:
+        vp, vs = _rows(v, "v", geom.Hkv, geom.Dv, n, dev)
+    if q is not None:
+        qp, qs = _rows(q, "q", geom.Hq, geom.Dk, n, dev)
+        if q_out is None:
+            q_out = torch.empty((n, geom.Hq, geom.Dk), dtype=q.dtype, device=dev)
+        qo = _need(q_out, "q_out", (n, geom.Hq, geom.Dk), _BF16, dev)
+        if n == 0:
+            qo = qp
+    else:
+        qo = None
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    fq = None if inv_freq is None else _need(inv_freq, "inv_freq", (rot // 2,),
+                                             (torch.float32,), dev)
+    ll = None if logical_lens is None else _need(logical_lens, "logical_lens", (geom.B,),
+                                                 (torch.int32,), dev)
+    s16 = None if summ is None else _need(summ, "summ", (geom.n_pool, geom.Hkv, 2, geom.Dk),
+                                          _BF16, dev)
+    s8 = None if summ8 is None else _need(
+        summ8, "summ8", (geom.n_pool, geom.Hkv, 2 * geom.Dk + 16), (torch.uint8,), dev)
+    g = geom.c()
+    with torch.cuda.device(dev):
+        _check(lib.sa_append_kv(ctypes.byref(g), qp, qs, kp, ks, vp, vs, n, cu, pt, sl, ll, fq,
+                                int(rot_start), rot, int(bool(interleaved)), qo, kc, vc, s16, s8,
+                                _ptr(ws.buf), ws.nbytes, _stream(stream)), "sa_append_kv")
+    return q_out if q is not None else None
+
+
+def attend_chunk(geom: Geometry, q, cu_new, k_cache, v_cache, page_table, seq_lens, scale,
+                 ws: Workspace, sink: int = 0, window: int = 0, out=None, lse=None, stream=None):
+    """Exact causal attention of the new tokens ``q`` [n, Hq, Dk] (rows
+    ``cu_new[b]:cu_new[b+1]`` are the last tokens of sequence b) over the paged cache, with
+    ``window`` > 0 restricted to ``sink`` first tokens and the last ``window`` ones.  Returns
+    (out [n, Hq, Dv] bf16, lse [n, Hq] fp32); rows of no sequence keep what they held."""
+    dev, n = k_cache.device, q.shape[0]
+    cu, pt, sl, kc, vc = _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, dev)
+    qp = _need(q, "q", (n, geom.Hq, geom.Dk), _BF16, dev)
+    if out is None:
+        out = torch.empty((n, geom.Hq, geom.Dv), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((n, geom.Hq), dtype=torch.float32, device=dev)
+    op = _need(out, "out", (n, geom.Hq, geom.Dv), _BF16, dev)
+    lp = _need(lse, "lse", (n, geom.Hq), (torch.float32,), dev)
+    if n == 0:
+        return out, lse
+    g = geom.c()
+    with torch.cuda.device(dev):
+        _check(lib.sa_attend_chunk(ctypes.byref(g), qp, n, cu, kc, vc, pt, sl, int(sink),
+                                   int(window), float(scale), op, lp, _ptr(ws.buf), ws.nbytes,
+                                   _stream(stream)), "sa_attend_chunk")
+    return out, lse

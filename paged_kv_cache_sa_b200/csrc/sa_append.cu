@@ -1,0 +1,425 @@
+// sa_append.cu -- new tokens' keys and values into the paged cache, with the position
+// rotation and the refresh of the touched pages' summaries.
+//
+// Method.  New token i of sequence b goes to slot s = L_b - n_b + i; its position is
+// p = (logical length or L_b) - n_b + i.  Rotation pairs (x, y) of a key or query row turn by
+// a = p * inv_freq[j]: (x cos a - y sin a, y cos a + x sin a).  p reaches millions, where an
+// fp32 product is off by up to 2^-24 * a (0.06 rad at a = 10^6): the angle is formed in fp64
+// as a number of turns, its whole turns are dropped there, and only the fraction (rounded
+// once, 2^-25 turns) goes to sincospif.  The rotation is fp32; the only rounding to bf16 is
+// the store.
+//
+// One CTA per (sequence, page that receives tokens): the page is the unit that has a single
+// owner, so the summaries (min/max over all valid rows of the page, the old ones read back
+// from the cache, the new ones still in registers) need no atomics and no second launch.
+// cos/sin of the page's new tokens are computed once into shared memory and serve every query
+// and key head.  A lane holds a "unit": two 16-byte chunks of one row that rotate together
+// (j and j + rot/2 in the half-split form, neighbours in the interleaved form), so loads and
+// stores stay 16 bytes wide and coalesced.  Bound by HBM: every row is read once and written
+// once.
+#include "sa_common.cuh"
+#include "sa_fp8.cuh"
+#include "sa_internal.h"
+
+namespace sa {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+
+struct AppendArgs {
+  const uint4* q;
+  const uint4* k;
+  const uint4* v;
+  int64_t q_stride, k_stride, v_stride;  // 16-byte chunks from one token to the next
+  const int32_t* cu_new;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* logical_lens;
+  const float* inv_freq;
+  uint4* q_out;
+  uint4* k_cache;
+  uint4* v_cache;
+  void* summ;
+  int32_t* status;
+  int n_tokens, B, Hq, Hkv, P, max_pages, n_pool;
+  int rot_start, rot_dim, interleaved;
+  int want;  // 0: no summaries, 1: bf16 rows, 2: fp8 records
+};
+
+// the two chunks of unit u of a row, and its first rotation pair (-1: not rotated)
+struct Unit {
+  int ca, cb, pair;
+};
+
+__device__ __forceinline__ Unit unit_of(int u, int rot_start, int rot_dim, bool interleaved) {
+  const int n_rot = rot_dim >> 4, c0 = rot_start >> 3;
+  Unit x;
+  if (u < n_rot) {
+    x.ca = interleaved ? c0 + 2 * u : c0 + u;
+    x.cb = interleaved ? x.ca + 1 : x.ca + n_rot;
+    x.pair = 8 * u;
+  } else {
+    x.ca = 2 * (u - n_rot);
+    x.cb = x.ca + 1;
+    if (x.ca >= c0) x.ca += 2 * n_rot;
+    if (x.cb >= c0) x.cb += 2 * n_rot;
+    x.pair = -1;
+  }
+  return x;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// (x, y) of both halves of two words turned by cs[0], cs[1]
+__device__ __forceinline__ void turn2(uint32_t& a, uint32_t& b, float2 t0, float2 t1) {
+  const float x0 = bf_lo(a), x1 = bf_hi(a), y0 = bf_lo(b), y1 = bf_hi(b);
+  a = pack_bf16(x0 * t0.x - y0 * t0.y, x1 * t1.x - y1 * t1.y);
+  b = pack_bf16(y0 * t0.x + x0 * t0.y, y1 * t1.x + x1 * t1.y);
+}
+__device__ __forceinline__ uint32_t turn_pair(uint32_t w, float2 t) {
+  const float x = bf_lo(w), y = bf_hi(w);
+  return pack_bf16(x * t.x - y * t.y, y * t.x + x * t.y);
+}
+
+__device__ __forceinline__ void rotate_unit(uint4& a, uint4& b, const float2* cs,
+                                            bool interleaved) {
+  if (!interleaved) {
+    turn2(a.x, b.x, cs[0], cs[1]);
+    turn2(a.y, b.y, cs[2], cs[3]);
+    turn2(a.z, b.z, cs[4], cs[5]);
+    turn2(a.w, b.w, cs[6], cs[7]);
+  } else {
+    a.x = turn_pair(a.x, cs[0]);
+    a.y = turn_pair(a.y, cs[1]);
+    a.z = turn_pair(a.z, cs[2]);
+    a.w = turn_pair(a.w, cs[3]);
+    b.x = turn_pair(b.x, cs[4]);
+    b.y = turn_pair(b.y, cs[5]);
+    b.z = turn_pair(b.z, cs[6]);
+    b.w = turn_pair(b.w, cs[7]);
+  }
+}
+
+// running min and max of a chunk, on the bf16 order keys
+struct Range {
+  uint4 mn, mx;
+  __device__ __forceinline__ void clear() {
+    mn = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+    mx = make_uint4(0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u);
+  }
+  __device__ __forceinline__ void merge(const uint4& lo, const uint4& hi) {
+    mn.x = __vmins2(mn.x, lo.x); mn.y = __vmins2(mn.y, lo.y);
+    mn.z = __vmins2(mn.z, lo.z); mn.w = __vmins2(mn.w, lo.w);
+    mx.x = __vmaxs2(mx.x, hi.x); mx.y = __vmaxs2(mx.y, hi.y);
+    mx.z = __vmaxs2(mx.z, hi.z); mx.w = __vmaxs2(mx.w, hi.w);
+  }
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint4 k = make_uint4(bf2_key(v.x), bf2_key(v.y), bf2_key(v.z), bf2_key(v.w));
+    merge(k, k);
+  }
+  __device__ __forceinline__ void merge_lane(int off) {
+    uint4 lo, hi;
+    lo.x = __shfl_xor_sync(0xffffffffu, mn.x, off); lo.y = __shfl_xor_sync(0xffffffffu, mn.y, off);
+    lo.z = __shfl_xor_sync(0xffffffffu, mn.z, off); lo.w = __shfl_xor_sync(0xffffffffu, mn.w, off);
+    hi.x = __shfl_xor_sync(0xffffffffu, mx.x, off); hi.y = __shfl_xor_sync(0xffffffffu, mx.y, off);
+    hi.z = __shfl_xor_sync(0xffffffffu, mx.z, off); hi.w = __shfl_xor_sync(0xffffffffu, mx.w, off);
+    merge(lo, hi);
+  }
+  __device__ __forceinline__ uint4 low() const {
+    return make_uint4(bf2_key(mn.x), bf2_key(mn.y), bf2_key(mn.z), bf2_key(mn.w));
+  }
+  __device__ __forceinline__ uint4 high() const {
+    return make_uint4(bf2_key(mx.x), bf2_key(mx.y), bf2_key(mx.z), bf2_key(mx.w));
+  }
+};
+
+// New tokens of sequence b: first row and count, or n = 0 (reported) when they do not fit.
+__device__ __forceinline__ void new_tokens(const int32_t* cu, const int32_t* lens, int b,
+                                           int n_tokens, int64_t cap, int32_t* status, int& c0,
+                                           int& n, int& L) {
+  c0 = cu[b];
+  const int c1 = cu[b + 1];
+  L = lens[b];
+  const bool ok = c0 >= 0 && c1 >= c0 && c1 <= n_tokens && L >= c1 - c0 && L <= cap;
+  n = ok ? c1 - c0 : 0;
+  if (!ok) report(status, SA_ERR_DEVICE_CHECK);
+}
+
+// CPR = 16-byte chunks per key row (Dk / 8).
+template <int CPR>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr int U = CPR / 2;  // units per row
+  extern __shared__ float2 cs[];  // [new tokens of the page][rot_dim / 2]
+  __shared__ int scan[kAppendWarps];
+  __shared__ int found[2];  // sequence and page of this CTA's item
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int half = a.rot_dim >> 1;
+  const bool inter = a.interleaved != 0;
+  const int64_t cap = (int64_t)a.max_pages * a.P;
+
+  for (int item = blockIdx.x;; item += gridDim.x) {
+    // ---- the item's sequence and page: running count of touched pages over the batch
+    if (tid == 0) found[0] = -1;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kAppendThreads) {
+      const int b = b0 + tid;
+      int pages = 0, first = 0;
+      if (b < a.B) {
+        int c0, n, L;
+        new_tokens(a.cu_new, a.seq_lens, b, a.n_tokens, cap, a.status, c0, n, L);
+        if (n > 0) {
+          first = (L - n) / a.P;
+          pages = (L - 1) / a.P - first + 1;
+        }
+      }
+      int incl = pages;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+      }
+      __syncthreads();  // scan[] of the previous round was read, found[] is cleared
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      int base = before, all = before;
+#pragma unroll
+      for (int w = 0; w < kAppendWarps; ++w) {
+        if (w < warp) base += scan[w];
+        all += scan[w];
+      }
+      const int lo = base + incl - pages;
+      if (item >= lo && item < lo + pages) {
+        found[0] = b;
+        found[1] = first + (item - lo);
+      }
+      before = all;
+      if (item < before) break;
+    }
+    __syncthreads();
+    const int b = found[0], lp = found[1];
+    if (b < 0) return;
+    const int c0 = a.cu_new[b], n = a.cu_new[b + 1] - c0, L = a.seq_lens[b];
+    const int page0 = lp * a.P, s0 = L - n;
+    const int t0 = max(s0, page0), t1 = min(L, page0 + a.P);
+    const int cnt = t1 - t0;           // new tokens of the page
+    const int row0 = c0 + (t0 - s0);   // their first input row
+    const int slot0 = t0 - page0;      // and slot; rows [0, slot0) are old
+    const int phys = a.page_table[(size_t)b * a.max_pages + lp];
+    if (phys < 0 || phys >= a.n_pool) {
+      if (tid == 0) report(a.status, SA_ERR_DEVICE_CHECK);
+      __syncthreads();
+      continue;
+    }
+    const int pos0 = (a.logical_lens ? a.logical_lens[b] : L) - n + (t0 - s0);
+    // ---- cos and sin of every (new token, pair)
+    for (int e = tid; e < cnt * half; e += kAppendThreads) {
+      const int i = e / half, j = e - i * half;
+      const double turns = (double)(pos0 + i) * (double)a.inv_freq[j] * 0.15915494309189535;
+      const float frac = (float)(2.0 * (turns - rint(turns)));  // half turns in [-1, 1]
+      float sn, co;
+      sincospif(frac, &sn, &co);
+      cs[e] = make_float2(co, sn);
+    }
+    __syncthreads();
+
+    // ---- keys: rotate and store the new rows, min/max over the page's valid rows
+    const int rows = slot0 + cnt;
+    const int from = a.want ? 0 : slot0;
+    if constexpr (32 % U == 0) {
+      const int u = lane % U, rg = lane / U;
+      constexpr int RPW = 32 / U;
+      const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
+      for (int h = blockIdx.y * kAppendWarps + warp; h < a.Hkv;
+           h += gridDim.y * kAppendWarps) {
+        uint4* blk = a.k_cache + ((size_t)phys * a.Hkv + h) * a.P * CPR;
+        Range ra, rb;
+        ra.clear();
+        rb.clear();
+#pragma unroll 4
+        for (int r = from + rg; r < rows; r += RPW) {
+          uint4 va, vb;
+          if (r < slot0) {
+            va = blk[r * CPR + x.ca];
+            vb = blk[r * CPR + x.cb];
+          } else {
+            const int i = r - slot0;
+            const uint4* src = a.k + (size_t)(row0 + i) * a.k_stride + h * CPR;
+            va = src[x.ca];
+            vb = src[x.cb];
+            if (x.pair >= 0) rotate_unit(va, vb, cs + i * half + x.pair, inter);
+            blk[r * CPR + x.ca] = va;
+            blk[r * CPR + x.cb] = vb;
+          }
+          ra.add(va);
+          rb.add(vb);
+        }
+        if (a.want) {
+#pragma unroll
+          for (int off = U; off < 32; off <<= 1) {
+            ra.merge_lane(off);
+            rb.merge_lane(off);
+          }
+          const size_t rec = (size_t)phys * a.Hkv + h;
+          const uint4 la = ra.low(), ha = ra.high(), lb = rb.low(), hb = rb.high();
+          if (a.want == 2) {
+            constexpr int D = CPR * 8;
+            uint32_t am = max_mag2(max_mag2(max_mag2(max_mag2(0u, la.x), la.y), la.z), la.w);
+            am = max_mag2(max_mag2(max_mag2(max_mag2(am, ha.x), ha.y), ha.z), ha.w);
+            am = max_mag2(max_mag2(max_mag2(max_mag2(am, lb.x), lb.y), lb.z), lb.w);
+            am = max_mag2(max_mag2(max_mag2(max_mag2(am, hb.x), hb.y), hb.z), hb.w);
+            am = __reduce_max_sync(0xffffffffu, am);
+            const int e = fp8_record_exp(am);
+            uint8_t* out = static_cast<uint8_t*>(a.summ) + rec * (2 * D + 16);
+            if (lane < U) {
+              *reinterpret_cast<uint2*>(out + x.ca * 8) =
+                  make_uint2(e4m3_pack(la.x, la.y, e, false), e4m3_pack(la.z, la.w, e, false));
+              *reinterpret_cast<uint2*>(out + x.cb * 8) =
+                  make_uint2(e4m3_pack(lb.x, lb.y, e, false), e4m3_pack(lb.z, lb.w, e, false));
+              *reinterpret_cast<uint2*>(out + D + x.ca * 8) =
+                  make_uint2(e4m3_pack(ha.x, ha.y, e, true), e4m3_pack(ha.z, ha.w, e, true));
+              *reinterpret_cast<uint2*>(out + D + x.cb * 8) =
+                  make_uint2(e4m3_pack(hb.x, hb.y, e, true), e4m3_pack(hb.z, hb.w, e, true));
+            }
+            if (lane == 0)
+              *reinterpret_cast<uint4*>(out + 2 * D) = make_uint4((uint32_t)e & 0xFFu, 0u, 0u, 0u);
+          } else if (lane < U) {
+            uint4* out = static_cast<uint4*>(a.summ) + rec * 2 * CPR;
+            out[x.ca] = la;
+            out[x.cb] = lb;
+            out[CPR + x.ca] = ha;
+            out[CPR + x.cb] = hb;
+          }
+        }
+      }
+    } else if (blockIdx.y == 0) {
+      // latent rows (one KV head): the CTA's row groups split the page's rows, their
+      // partial ranges meet in shared memory
+      constexpr int NG = kAppendThreads / U;
+      __shared__ Range part[NG][CPR];
+      const int u = tid % U, rg = tid / U;
+      const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
+      uint4* blk = a.k_cache + (size_t)phys * a.P * CPR;
+      Range ra, rb;
+      ra.clear();
+      rb.clear();
+      if (rg < NG) {
+#pragma unroll 4
+        for (int r = from + rg; r < rows; r += NG) {
+          uint4 va, vb;
+          if (r < slot0) {
+            va = blk[r * CPR + x.ca];
+            vb = blk[r * CPR + x.cb];
+          } else {
+            const int i = r - slot0;
+            const uint4* src = a.k + (size_t)(row0 + i) * a.k_stride;
+            va = src[x.ca];
+            vb = src[x.cb];
+            if (x.pair >= 0) rotate_unit(va, vb, cs + i * half + x.pair, inter);
+            blk[r * CPR + x.ca] = va;
+            blk[r * CPR + x.cb] = vb;
+          }
+          ra.add(va);
+          rb.add(vb);
+        }
+        if (a.want) {
+          part[rg][x.ca] = ra;
+          part[rg][x.cb] = rb;
+        }
+      }
+      if (a.want) {
+        __syncthreads();
+        if (tid < CPR) {
+          Range r = part[0][tid];
+          for (int g = 1; g < NG; ++g) r.merge(part[g][tid].mn, part[g][tid].mx);
+          uint4* out = static_cast<uint4*>(a.summ) + (size_t)phys * 2 * CPR;
+          out[tid] = r.low();
+          out[CPR + tid] = r.high();
+        }
+      }
+    }
+
+    // ---- queries: (token, head) rows of the page's new tokens, all threads of the column
+    const int first = blockIdx.y * kAppendThreads + tid, step = gridDim.y * kAppendThreads;
+    if (a.q) {
+      const int n_e = cnt * a.Hq * U;
+#pragma unroll 4
+      for (int e = first; e < n_e; e += step) {
+        const int row = e / U, u = e % U;
+        const int i = row / a.Hq, h = row - i * a.Hq;
+        const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
+        const uint4* src = a.q + (size_t)(row0 + i) * a.q_stride + h * CPR;
+        uint4 va = src[x.ca], vb = src[x.cb];
+        if (x.pair >= 0) rotate_unit(va, vb, cs + i * half + x.pair, inter);
+        uint4* dst = a.q_out + ((size_t)(row0 + i) * a.Hq + h) * CPR;
+        dst[x.ca] = va;
+        dst[x.cb] = vb;
+      }
+    }
+    // ---- values: plain rows into their slots
+    if (a.v) {
+      const int n_e = a.Hkv * cnt * CPR;
+#pragma unroll 4
+      for (int e = first; e < n_e; e += step) {
+        const int row = e / CPR, c = e % CPR;
+        const int h = row / cnt, i = row - h * cnt;
+        a.v_cache[(((size_t)phys * a.Hkv + h) * a.P + slot0 + i) * CPR + c] =
+            a.v[(size_t)(row0 + i) * a.v_stride + h * CPR + c];
+      }
+    }
+    __syncthreads();  // cs[] and found[] are free for the next item
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t stream) {
+  AppendArgs a;
+  a.q = static_cast<const uint4*>(c.q);
+  a.k = static_cast<const uint4*>(c.k);
+  a.v = static_cast<const uint4*>(c.v);
+  a.q_stride = c.q_stride / 8;
+  a.k_stride = c.k_stride / 8;
+  a.v_stride = c.v_stride / 8;
+  a.cu_new = c.cu_new;
+  a.page_table = c.page_table;
+  a.seq_lens = c.seq_lens;
+  a.logical_lens = c.logical_lens;
+  a.inv_freq = c.inv_freq;
+  a.q_out = static_cast<uint4*>(c.q_out);
+  a.k_cache = static_cast<uint4*>(c.k_cache);
+  a.v_cache = static_cast<uint4*>(c.v_cache);
+  a.summ = c.summ8 ? c.summ8 : c.summ;
+  a.status = c.status;
+  a.n_tokens = c.n_tokens;
+  a.B = g.B;
+  a.Hq = g.Hq;
+  a.Hkv = g.Hkv;
+  a.P = g.P;
+  a.max_pages = g.max_pages;
+  a.n_pool = g.n_pool;
+  a.rot_start = c.rot_start;
+  a.rot_dim = c.rot_dim;
+  a.interleaved = c.interleaved;
+  a.want = c.summ8 ? 2 : c.summ ? 1 : 0;
+  // pages that n_tokens new tokens of min(B, n_tokens) sequences can touch: a run of n
+  // tokens touches at most (n - 1) / P + 2 pages and no more than n
+  const int64_t nseq = g.B < c.n_tokens ? g.B : c.n_tokens;
+  int64_t items = c.n_tokens / g.P + 2 * nseq;
+  if (items > c.n_tokens) items = c.n_tokens;
+  if (items > 65535) items = 65535;  // the kernel strides over the rest
+  const int split = items >= 296 ? 1 : items >= 148 ? 2 : 4;
+  const dim3 grid((unsigned)items, split), block(kAppendThreads);
+  const size_t smem = (size_t)g.P * (c.rot_dim / 2) * sizeof(float2);  // at most 32 KB
+  switch (g.Dk) {
+    case 64: append_kernel<8><<<grid, block, smem, stream>>>(a); break;
+    case 128: append_kernel<16><<<grid, block, smem, stream>>>(a); break;
+    case 576: append_kernel<72><<<grid, block, smem, stream>>>(a); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace sa

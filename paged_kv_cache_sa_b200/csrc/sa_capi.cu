@@ -153,7 +153,7 @@ SA_EXPORT const char* sa_status_string(int status) {
   }
 }
 
-SA_EXPORT int sa_version(void) { return 10000; }
+SA_EXPORT int sa_version(void) { return 10100; }
 
 SA_EXPORT size_t sa_decode_workspace_size(const sa_geom* g, int budget) {
   if (check_geom(g) != SA_OK || budget < g->P || budget % g->P) return 0;
@@ -591,4 +591,102 @@ SA_EXPORT int sa_prune_compact(const sa_geom* g, const void* k_cache, const void
   return cuda_status(launch_prune(*g, k_cache, v_cache, page_table, seq_lens, keep, free_pages,
                                   n_free, k_dst, v_dst, summ, new_page_table, new_seq_lens,
                                   pos_map, logical_len, ws, static_cast<cudaStream_t>(stream)));
+}
+
+SA_EXPORT int sa_append_kv(const sa_geom* g, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, int n_tokens,
+                           const int32_t* cu_new, const int32_t* page_table,
+                           const int32_t* seq_lens, const int32_t* logical_lens,
+                           const float* inv_freq, int rot_start, int rot_dim, int interleaved,
+                           void* q_out, void* k_cache, void* v_cache, void* summ, void* summ8,
+                           void* ws, size_t ws_bytes, void* stream) {
+  int st = check_geom(g);
+  if (st != SA_OK) return st;
+  const bool latent = is_latent(*g);
+  if (n_tokens < 0 || !k || !cu_new || !page_table || !seq_lens || !k_cache)
+    return SA_ERR_INVALID_ARG;
+  if (!latent && (!v || !v_cache)) return SA_ERR_INVALID_ARG;
+  if (q && !q_out) return SA_ERR_INVALID_ARG;
+  if (summ && summ8) return SA_ERR_INVALID_ARG;
+  if (summ8 && (latent || !score_supported_fp8(*g))) return SA_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_start < 0 || rot_dim % 16 || rot_start % 8 ||
+      (int64_t)rot_start + rot_dim > g->Dk || (rot_dim > 0 && !inv_freq))
+    return SA_ERR_INVALID_ARG;
+  if (rot_dim > 128) return SA_ERR_UNSUPPORTED;
+  // row strides: a 16-byte vector never straddles a row, and rows do not overlap
+  if (k_stride % 8 || k_stride < (int64_t)g->Hkv * g->Dk) return SA_ERR_INVALID_ARG;
+  if (!latent && (v_stride % 8 || v_stride < (int64_t)g->Hkv * g->Dv)) return SA_ERR_INVALID_ARG;
+  if (q && (q_stride % 8 || q_stride < (int64_t)g->Hq * g->Dk)) return SA_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != (int64_t)g->Hq * g->Dk) return SA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(k_cache) || (q && (!aligned16(q) || !aligned16(q_out))) ||
+      (!latent && (!aligned16(v) || !aligned16(v_cache))) || !aligned16(summ) ||
+      !aligned16(summ8))
+    return SA_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < 256 || !aligned16(ws)) return SA_ERR_WORKSPACE;
+  if (n_tokens == 0) return SA_OK;
+  AppendCall c;
+  c.q = q;
+  c.k = k;
+  c.v = latent ? nullptr : v;
+  c.q_stride = q_stride;
+  c.k_stride = k_stride;
+  c.v_stride = v_stride;
+  c.n_tokens = n_tokens;
+  c.cu_new = cu_new;
+  c.page_table = page_table;
+  c.seq_lens = seq_lens;
+  c.logical_lens = logical_lens;
+  c.inv_freq = inv_freq;
+  c.rot_start = rot_start;
+  c.rot_dim = rot_dim;
+  c.interleaved = interleaved != 0;
+  c.q_out = q_out;
+  c.k_cache = k_cache;
+  c.v_cache = v_cache;
+  c.summ = summ;
+  c.summ8 = summ8;
+  c.status = &static_cast<WsHeader*>(ws)->status_bits;
+  return cuda_status(launch_append(*g, c, static_cast<cudaStream_t>(stream)));
+}
+
+SA_EXPORT size_t sa_chunk_workspace_size(const sa_geom* g, int n_tokens) {
+  if (check_geom(g) != SA_OK || n_tokens < 0) return 0;
+  return 256 + chunk_workspace_bytes(*g, n_tokens, sm_count());
+}
+
+SA_EXPORT int sa_attend_chunk(const sa_geom* g, const void* q, int n_tokens,
+                              const int32_t* cu_new, const void* k_cache, const void* v_cache,
+                              const int32_t* page_table, const int32_t* seq_lens, int sink,
+                              int window, float scale, void* out, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+  int st = check_geom(g);
+  if (st != SA_OK) return st;
+  if (n_tokens < 0 || !q || !cu_new || !k_cache || !page_table || !seq_lens || !out || !lse)
+    return SA_ERR_INVALID_ARG;
+  if (!g->v_aliases_k && !v_cache) return SA_ERR_INVALID_ARG;
+  if (sink < 0 || window < 0 || !(scale > 0.f) || !(scale < 3.0e38f)) return SA_ERR_INVALID_ARG;
+  const void* vc = g->v_aliases_k ? k_cache : v_cache;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(vc) || !aligned16(out))
+    return SA_ERR_INVALID_ARG;
+  const int n_sm = sm_count();
+  if (!ws || !aligned16(ws) || ws_bytes < 256 + chunk_workspace_bytes(*g, n_tokens, n_sm))
+    return SA_ERR_WORKSPACE;
+  if (n_tokens == 0) return SA_OK;
+  ChunkCall c;
+  c.q = q;
+  c.n_tokens = n_tokens;
+  c.cu_new = cu_new;
+  c.k_cache = k_cache;
+  c.v_cache = vc;
+  c.page_table = page_table;
+  c.seq_lens = seq_lens;
+  c.sink = sink;
+  c.window = window;
+  c.scale = scale;
+  c.out = out;
+  c.lse = lse;
+  c.scratch = static_cast<uint8_t*>(ws) + 256;
+  c.status = &static_cast<WsHeader*>(ws)->status_bits;
+  c.n_sm = n_sm;
+  return cuda_status(launch_chunk(*g, c, static_cast<cudaStream_t>(stream)));
 }

@@ -131,6 +131,48 @@ cudaError_t launch_prune(const sa_geom& g, const void* k_cache, const void* v_ca
 
 size_t prune_workspace_bytes(const sa_geom& g);
 
+// Appending new tokens' rows to the cache (rotation and summary refresh included).
+struct AppendCall {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+  int n_tokens;
+  const int32_t* cu_new;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* logical_lens;  // nullable
+  const float* inv_freq;
+  int rot_start, rot_dim, interleaved;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  void* summ;   // bf16 summaries (nullable)
+  void* summ8;  // fp8 records (nullable)
+  int32_t* status;
+};
+cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t stream);
+
+// Attention of a ragged chunk of new tokens over the paged cache.
+struct ChunkCall {
+  const void* q;
+  int n_tokens;
+  const int32_t* cu_new;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  int sink, window;
+  float scale;
+  void* out;
+  float* lse;
+  uint8_t* scratch;  // workspace behind the header, chunk_workspace_bytes
+  int32_t* status;
+  int n_sm;
+};
+size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm);
+cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream);
+
 // TMA descriptor encoder from the driver (resolved once through the runtime).
 bool encode_rows_tmap(void* tmap_out, const void* base, uint64_t inner_elems, uint64_t rows,
                       uint32_t box_inner, uint32_t box_rows);
