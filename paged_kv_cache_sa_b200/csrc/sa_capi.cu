@@ -116,6 +116,24 @@ bool encode_rows_tmap(void* tmap_out, const void* base, uint64_t inner_elems, ui
   return r == CUDA_SUCCESS;
 }
 
+// 3-D bf16 tensor [tokens][heads][inner] (dense), 128-byte swizzle (box_inner * 2 is 128): a
+// box lands as box_tokens * box_heads rows of 128 bytes, zero-filled outside the tensor.
+bool encode_heads_tmap(void* tmap_out, const void* base, uint64_t inner, uint64_t heads,
+                       uint64_t tokens, uint32_t box_inner, uint32_t box_heads,
+                       uint32_t box_tokens) {
+  auto fn = get_encode();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, heads, tokens};
+  cuuint64_t strides[2] = {inner * 2, inner * heads * 2};
+  cuuint32_t box[3] = {box_inner, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(static_cast<CUtensorMap*>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 3-D view of a [rows][128] bf16 pool as (64 channels, rows, 2 halves of a row): one box
 // of {64, box_rows, 2} lands as [half][row][64] with the 128-byte swizzle, the layout of
 // two 2-D boxes of {64, box_rows}.
@@ -687,6 +705,7 @@ SA_EXPORT int sa_attend_chunk(const sa_geom* g, const void* q, int n_tokens,
   c.lse = lse;
   c.scratch = static_cast<uint8_t*>(ws) + 256;
   c.status = &static_cast<WsHeader*>(ws)->status_bits;
+  c.ticket = &static_cast<WsHeader*>(ws)->pad[1];
   c.n_sm = n_sm;
   return cuda_status(launch_chunk(*g, c, static_cast<cudaStream_t>(stream)));
 }

@@ -1,116 +1,725 @@
-// sa_chunk.cu -- exact attention of a ragged chunk of new tokens over the paged cache.
+// sa_chunk.cu -- exact attention of a ragged chunk of new tokens over the paged cache,
+// grouped-query geometry, on the 5th-generation tensor cores.
 //
 // Method: x_t = scale q . k_t over the tokens t a query sees, one pass over the keys with the
-// running maximum m and sum l of the softmax: out = sum 2^(x_t - m) v_t / l.
-// One warp per (row, query head), lanes split the channels.
-#include "sa_common.cuh"
+// running maximum m and sum l of the softmax: out = sum 2^(x_t - m) v_t / l  (x in base 2).
+//
+// Rows.  The G query heads of a KV head see the same keys, so a matrix tile of 128 rows is
+// 128 / G tokens times G heads, and K and V are read once for all of them.
+// A CTA holds two accumulators (O0, O1) and two score tiles (S0, S1) in tensor memory, all
+// 512 columns at Dk = 128:
+//   a full block: two row tiles against one key tile per step (every K and V tile staged in
+//   shared memory serves 256 rows);
+//   a short block (the rows fit one tile: decode rows, drafts, the end of a prompt): one row
+//   tile against two key tiles per step, even ones in (S0, O0) and odd ones in (S1, O1), each
+//   with its own m and l, joined at the end.  The work per step is the same, so a single
+//   token still keeps two chains of products and exponentials in flight; the rows that are
+//   padding cost tensor time (1024 cycles per 64 KB key tile), which HBM hides (2800 cycles).
+// Per tile: S = Q K^T (128 x 128 x Dk) from shared memory; four softmax warps (thread = row)
+// read S, subtract the row's maximum, write P in bf16 over S's columns and O += P V
+// (128 x Dv x 128) takes P from tensor memory.  While one chain's softmax runs, the other
+// chain's two products do.
+// The maximum in use is only raised when a row's new maximum exceeds it by more than 2^8
+// (P then stays below 2^8, exact in range for bf16 and fp32): O is rescaled a few times per
+// row instead of at every tile, by the softmax warps themselves.
+// Warps 0-3 and 4-7: softmax of chain 0 and 1; 8: issues the products; 9: work list and TMA.
+#include "sa_chunk.cuh"
 #include "sa_internal.h"
+#include "sa_tc.cuh"
 
 namespace sa {
 
-namespace {
+namespace chunk {
 
-struct ChunkArgs {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  const int32_t* cu_new;
+constexpr int kThreads = 320;
+constexpr int kSegs = 2;
+constexpr uint32_t kHalfBytes = kKeyTile * 128;  // 128 rows of 64 channels
+
+template <int D>
+struct Lay {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kRing = 2 * kTileBytes;
+  static constexpr uint32_t kMisc = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kSmem = kMisc + 3072;
+};
+
+struct Misc {
+  float2 ml[2][128];  // (m, l) of both chains, short blocks
+  ChunkSeg seg[kSegs];
+  uint64_t full[10], empty[10];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], meet, drain;
+  uint32_t tmem;
+  int quit;
+};
+static_assert(sizeof(Misc) <= 3072, "misc area");
+
+struct Args {
+  ChunkShape shape;
   const int32_t* page_table;
-  const int32_t* seq_lens;
   uint16_t* out;
   float* lse;
-  int32_t* status;
-  int n_tokens, B, Hq, Hkv, P, max_pages, n_pool, sink, window;
+  float* part_o;    // [2 n_cta][rows_cap][D]
+  float2* part_ml;  // [2 n_cta][rows_cap]
+  ChunkCut* cut;    // [n_cta]
+  int rows_cap;
+  int Hq, Hkv, G, TB, P, page_shift, max_pages, n_pool;
   float scale_log2;
 };
 
-__device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-
-template <int DK, int DV>
-__global__ void __launch_bounds__(256) attend_chunk_kernel(const ChunkArgs a) {
-  constexpr int NK = DK / 32, NV = DV / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int row = (int)(w / a.Hq), hq = (int)(w % a.Hq), h = hq / (a.Hq / a.Hkv);
-  if (row >= a.n_tokens) return;
-  int b = -1;
-  for (int i = 0; i < a.B; ++i) {
-    const int c0 = a.cu_new[i], c1 = a.cu_new[i + 1], L = a.seq_lens[i];
-    if (!(c0 >= 0 && c1 >= c0 && c1 <= a.n_tokens && L >= c1 - c0 &&
-          L <= (int64_t)a.max_pages * a.P)) {
-      if (lane == 0) report(a.status, SA_ERR_DEVICE_CHECK);
-    } else if (row >= c0 && row < c1) {
-      b = i;
-    }
-  }
-  if (b < 0) return;
-  const int slot = a.seq_lens[b] - a.cu_new[b + 1] + row;
-  float q[NK], o[NV], m = -INFINITY, l = 0.f;
-  for (int j = 0; j < NK; ++j) q[j] = bf(a.q[((size_t)row * a.Hq + hq) * DK + lane + 32 * j]);
-  for (int j = 0; j < NV; ++j) o[j] = 0.f;
-  for (int t = 0; t <= slot; ++t) {
-    if (a.window > 0 && t >= a.sink && t <= slot - a.window) {
-      t = slot - a.window;
-      continue;
-    }
-    const int ph = a.page_table[(size_t)b * a.max_pages + t / a.P];
-    if (ph < 0 || ph >= a.n_pool) {
-      if (lane == 0) report(a.status, SA_ERR_DEVICE_CHECK);
-      continue;
-    }
-    const size_t r = ((size_t)ph * a.Hkv + h) * a.P + t % a.P;
-    float x = 0.f;
-    for (int j = 0; j < NK; ++j) x += q[j] * bf(a.k[r * DK + lane + 32 * j]);
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x), alpha = fast_exp2(m - mn), p = fast_exp2(x - mn);
-    m = mn;
-    l = l * alpha + p;
-    const uint16_t* vr = DK == DV ? a.v + r * DV : a.k + r * DK;
-    for (int j = 0; j < NV; ++j) o[j] = o[j] * alpha + p * bf(vr[lane + 32 * j]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int j = 0; j < NV; ++j)
-    a.out[((size_t)row * a.Hq + hq) * DV + lane + 32 * j] =
-        (uint16_t)(pack_bf16(o[j] * inv, 0.f) & 0xFFFFu);
-  if (lane == 0)
-    a.lse[(size_t)row * a.Hq + hq] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+__device__ __forceinline__ int tile_of(const ChunkSeg& g, int i) {
+  return i < g.na ? i : i - g.na + g.bs;
 }
 
-}  // namespace
+// ---- the producer warp: work list, queries and the ring of K and V tiles ---------------
+template <int D>
+__device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
+                                        const CUtensorMap* qmap, const CUtensorMap* kmap,
+                                        const CUtensorMap* vmap) {
+  using Y = Lay<D>;
+  const int lane = threadIdx.x & 31;
+  ChunkSched sched;
+  if (lane == 0) a.cut[blockIdx.x].nparts = 0;
+  sched.init(a.shape, blockIdx.x, gridDim.x);
+  const int ppt = kKeyTile >> a.page_shift;  // pages per tile
+  const int my_page = lane % ppt, my_half = lane / ppt;
+  const bool loads = my_half < Y::kHalves;
+  int it = 0;
+  bool ok = true;
+  for (int n = 0;; ++n) {
+    const int slot = n % kSegs;
+    if (n >= kSegs && !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit,
+                                     a.shape.status)) {
+      ok = false;
+      break;
+    }
+    ChunkSeg g;
+    const bool more = sched.next(g);
+    if (!more) g.valid = 0;
+    g.it0 = it;
+    if (lane == 0) {
+      mi.seg[slot] = g;
+      mbar_arrive(&mi.seg_full[slot]);
+      if (more && g.nparts > 0) a.cut[blockIdx.x] = ChunkCut{g.nparts, g.row0, g.ntok, g.h};
+    }
+    if (!more) break;
+    // queries: the box is G heads of TB tokens; rows behind the block belong to other
+    // sequences (or none) and their results are not kept
+    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, a.shape.status)) {
+      ok = false;
+      break;
+    }
+    const int ntile = g.split ? 1 : 2;
+    if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, ntile * Y::kHalves * a.TB * a.G * 128);
+    __syncwarp();
+    if (lane < ntile * Y::kHalves) {
+      const int t = lane / Y::kHalves, hf = lane % Y::kHalves;
+      tc::tma_3d(smem + Y::kQ + t * Y::kTileBytes + hf * kHalfBytes, qmap, hf * 64, g.h * a.G,
+                 g.row0 + t * a.TB, &mi.q_full);
+    }
+    // K and V tiles: K of the first tile(s), then V of a tile and K of the next without one
+    const int nt = g.i1 - g.i0, ahead = g.split ? 2 : 1;
+    const int s_hi = g.s0 + g.ntok - 1;
+    const int last_page = (g.L - 1) >> a.page_shift;
+    const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
+    // first page that any row's window reaches; pages of the sink below it
+    const int win_page =
+        a.shape.window > 0 ? max(0, g.s0 - a.shape.window + 1) >> a.page_shift : 0;
+    const int sink_pages = (a.shape.sink + (1 << a.page_shift) - 1) >> a.page_shift;
+    // physical page of this lane's part of tile i of the piece: -1 nothing to load there
+    auto lookup = [&](int i) -> int {
+      if (i >= nt) return -1;
+      const int kt = tile_of(g, g.i0 + i);
+      const int lp = kt * ppt + my_page;
+      if (!loads || lp > last_page || (lp << a.page_shift) > (s_hi | (kKeyTile - 1))) return -1;
+      if (lp < win_page && lp >= sink_pages) return -1;
+      const int ph = row[lp];
+      if (ph < 0 || ph >= a.n_pool) {
+        if ((lp << a.page_shift) <= s_hi) report(a.shape.status, SA_ERR_DEVICE_CHECK);
+        return -1;
+      }
+      return ph;
+    };
+    auto load = [&](const CUtensorMap* map, int ph) -> bool {
+      const int st = it % Y::kStages;
+      if (it >= Y::kStages && !tc::wait_warp(&mi.empty[st], (it / Y::kStages - 1) & 1, &mi.quit,
+                                             a.shape.status))
+        return false;
+      const unsigned m = __ballot_sync(0xffffffffu, ph >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(&mi.full[st], __popc(m) * a.P * 128);
+      __syncwarp();
+      if (ph >= 0)
+        tc::tma_2d(smem + Y::kRing + st * Y::kTileBytes + my_half * kHalfBytes +
+                       ((uint32_t)my_page << a.page_shift) * 128,
+                   map, my_half * 64, (ph * a.Hkv + g.h) << a.page_shift, &mi.full[st]);
+      ++it;
+      return true;
+    };
+    int p0 = lookup(0), p1 = lookup(1), p2 = lookup(2), p3 = lookup(3);
+    ok = load(kmap, p0);
+    if (ok && ahead == 2 && nt > 1) ok = load(kmap, p1);
+    for (int i = 0; ok && i < nt; ++i) {
+      const int p4 = lookup(i + 4);
+      ok = load(vmap, p0);
+      if (ok && i + ahead < nt) ok = load(kmap, ahead == 1 ? p1 : p2);
+      p0 = p1;
+      p1 = p2;
+      p2 = p3;
+      p3 = p4;
+    }
+    if (!ok) break;
+  }
+  if (!ok) {  // given up: let copies in flight land (bounded) before shared memory goes away
+    for (int x = max(0, it - Y::kStages); x < it; ++x)
+      mbar_wait(&mi.full[x % Y::kStages], (x / Y::kStages) & 1);
+    mbar_wait(&mi.q_full, 0);
+  }
+}
 
-size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm) { return 0; }
+// ---- one thread issues every product ----------------------------------------------------
+template <int D>
+__device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem) {
+  using Y = Lay<D>;
+  constexpr uint32_t id_s = tc::idesc(128, kKeyTile, false, false);
+  constexpr uint32_t id_o = tc::idesc(128, D, false, true);
+  int32_t* status = a.shape.status;
+  int it = 0, np[2] = {0, 0};
+  auto staged = [&](int x) {
+    const bool r = tc::wait(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status);
+    tc::fence_after();
+    return r;
+  };
+  auto scores = [&](int qt, int t, int x) {  // S_t = Q_qt K^T of stage x
+    const uint32_t q = smem + Y::kQ + qt * Y::kTileBytes;
+    const uint32_t k = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+      tc::mma_ss(tmem + t * 128, tc::desc(q + o), tc::desc(k + o), id_s, kk != 0);
+    }
+    tc::commit(&mi.s_full[t]);
+  };
+  auto values = [&](int t, int x, bool first) -> bool {  // O_t += P_t V of stage x
+    const bool r = tc::wait(&mi.p_full[t], np[t]++ & 1, &mi.quit, status);
+    tc::fence_after();
+    if (!r) return false;
+    const uint32_t v = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
+#pragma unroll
+    for (int kk = 0; kk < kKeyTile / 16; ++kk)
+      tc::mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8,
+                 tc::desc(v + kk * 2048, kHalfBytes), id_o, !(first && kk == 0));
+    return true;
+  };
+  for (int n = 0;; ++n) {
+    const int slot = n % kSegs;
+    if (!tc::wait(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
+    const bool valid = mi.seg[slot].valid != 0, split = mi.seg[slot].split != 0;
+    const int nt = mi.seg[slot].i1 - mi.seg[slot].i0;
+    mbar_arrive(&mi.seg_empty[slot]);
+    if (!valid) return;
+    if (!tc::wait(&mi.q_full, n & 1, &mi.quit, status)) return;
+    if (!split) {
+      int k = it++;
+      if (!staged(k)) return;
+      scores(0, 0, k);
+      scores(1, 1, k);
+      tc::commit(&mi.empty[k % Y::kStages]);
+      if (nt == 1) tc::commit(&mi.q_empty);
+      for (int i = 0; i < nt; ++i) {
+        const int v = it++;
+        const bool more = i + 1 < nt;
+        if (!staged(v) || !values(0, v, i == 0)) return;
+        if (more) {
+          k = it++;
+          if (!staged(k)) return;
+          scores(0, 0, k);
+        } else {
+          tc::commit(&mi.o_full[0]);
+        }
+        if (!values(1, v, i == 0)) return;
+        tc::commit(&mi.empty[v % Y::kStages]);
+        if (more) {
+          scores(1, 1, k);
+          tc::commit(&mi.empty[k % Y::kStages]);
+          if (i + 2 == nt) tc::commit(&mi.q_empty);
+        } else {
+          tc::commit(&mi.o_full[1]);
+        }
+      }
+    } else {
+      for (int i = 0; i < min(nt, 2); ++i) {
+        const int k = it++;
+        if (!staged(k)) return;
+        scores(0, i, k);
+        tc::commit(&mi.empty[k % Y::kStages]);
+        if (i + 1 == nt) tc::commit(&mi.q_empty);
+      }
+      for (int i = 0; i < nt; ++i) {
+        const int t = i & 1, v = it++;
+        if (!staged(v) || !values(t, v, i < 2)) return;
+        tc::commit(&mi.empty[v % Y::kStages]);
+        if (i + 2 < nt) {
+          const int k = it++;
+          if (!staged(k)) return;
+          scores(0, t, k);
+          tc::commit(&mi.empty[k % Y::kStages]);
+          if (i + 3 == nt) tc::commit(&mi.q_empty);
+        } else {
+          tc::commit(&mi.o_full[t]);
+        }
+      }
+    }
+  }
+}
 
-cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream) {
-  ChunkArgs a;
-  a.q = static_cast<const uint16_t*>(c.q);
-  a.k = static_cast<const uint16_t*>(c.k_cache);
-  a.v = static_cast<const uint16_t*>(c.v_cache);
-  a.cu_new = c.cu_new;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return fmaxf(fmaxf(a, b), c);
+}
+
+// ---- softmax and epilogue of chain t (four warps, thread = row) --------------------------
+template <int D>
+__device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem,
+                                       int t) {
+  using Y = Lay<D>;
+  const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3;
+  const int r = wq * 32 + lane;  // row of the tile = lane of tensor memory
+  const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+  const uint32_t s_col = tmem + lanes + t * 128;
+  const int tok = r / a.G, gh = r - tok * a.G;
+  int32_t* status = a.shape.status;
+  int ns = 0, no[2] = {0, 0}, nmeet = 0;
+  for (int n = 0;; ++n) {
+    const int slot = n % kSegs;
+    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
+    const ChunkSeg g = mi.seg[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&mi.seg_empty[slot]);
+    if (!g.valid) return;
+    const int nt = g.i1 - g.i0;
+    const int mine = g.split ? (nt + 1 - t) >> 1 : nt;  // tiles of this chain
+    const int tk = g.split ? tok : tok + t * a.TB;      // token of this row in the block
+    const bool real = tok < a.TB && tk < g.ntok;
+    const bool any = __any_sync(0xffffffffu, real);
+    const int s = real ? g.s0 + tk : 0x3FFFFFFF;  // its slot (padding rows: no mask, unused)
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < mine; ++i) {
+      const int ti = g.split ? 2 * i + t : i;
+      const int key0 = tile_of(g, g.i0 + ti) * kKeyTile;
+      if (!tc::wait_warp(&mi.s_full[t], ns++ & 1, &mi.quit, status)) return;
+      tc::fence_after();
+      // V rows that no page was loaded for, or that lie behind the sequence's end, would meet
+      // a probability of zero; they are zeroed because 0 * NaN is not
+      const int lo_row =
+          a.shape.window > 0 && key0 >= a.shape.sink
+              ? ((max(0, g.s0 - a.shape.window + 1) >> a.page_shift) << a.page_shift) - key0
+              : 0;
+      const bool ragged = key0 + kKeyTile > g.L || lo_row > 0 ||
+                          (a.shape.window > 0 && key0 < a.shape.sink);
+      if (ragged && (g.split || t == 0)) {
+        const int x = g.it0 + (g.split ? (ti + 1 < nt ? 2 + 2 * ti : 2 * nt - 1) : 1 + 2 * ti);
+        if (!tc::wait_warp(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status))
+          return;
+        const int key = key0 + r, page = key >> a.page_shift;
+        const bool in_window =
+            a.shape.window == 0 ||
+            page >= (max(0, g.s0 - a.shape.window + 1) >> a.page_shift) ||
+            page < ((a.shape.sink + (1 << a.page_shift) - 1) >> a.page_shift);
+        if (key >= g.L || !in_window) {
+          const uint32_t base = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes + r * 128;
+#pragma unroll
+          for (int e = 0; e < Y::kHalves * 8; ++e)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             base + (e >> 3) * kHalfBytes + (e & 7) * 16),
+                         "r"(0)
+                         : "memory");
+        }
+        tc::fence_async_smem();
+      }
+      if (any) {
+        uint32_t x[128];
+        tc::tmem_ld128(s_col, x);
+        const int hi = s - key0, lo = a.shape.window > 0 ? hi - a.shape.window : -1;
+        const int sk = a.shape.sink - key0;
+        // some key of the tile hidden from some row of the warp
+        if (__any_sync(0xffffffffu, real && (hi < kKeyTile - 1 || (lo >= 0 && sk <= min(lo, kKeyTile - 1))))) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (!(c <= hi && (c > lo || c < sk))) x[c] = 0xFF800000u;  // -inf
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 2)
+          mx = max3(mx, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        mx *= a.scale_log2;
+        if (i == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, real && mx - m > 8.f)) {
+          const float up = fmaxf(m, mx);
+          const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
+          m = up;
+          l *= f;
+          const uint32_t o_col = tmem + lanes + 256 + t * D;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_col + c0, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tc::tmem_st32(o_col + c0, o);
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float p0 =
+                fast_exp2(fmaf(__uint_as_float(x[c0 + c]), a.scale_log2, off));
+            const float p1 =
+                fast_exp2(fmaf(__uint_as_float(x[c0 + c + 1]), a.scale_log2, off));
+            sum[(c >> 1) & 1] += p0;
+            sum[((c >> 1) & 1) + 2] += p1;
+            p[c >> 1] = pack_bf16(p0, p1);
+          }
+          tc::tmem_st32(s_col + (c0 >> 1), p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::tmem_wait_st();
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mi.p_full[t]);
+    }
+    // ---- results: whole items are normalised and rounded, pieces leave (O, m, l)
+    const size_t orow = ((size_t)(g.row0 + tk) * a.Hq + g.h * a.G + gh);
+    const size_t prow = (size_t)max(g.part, 0) * a.rows_cap + (g.split ? 0 : t * 128) + r;
+    if (!g.split) {
+      if (!tc::wait_warp(&mi.o_full[t], no[t]++ & 1, &mi.quit, status)) return;
+      ++no[1 - t];  // the other chain's completes too; its warps wait for it
+      tc::fence_after();
+      if (any) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(tmem + lanes + 256 + t * D + c0, o);
+          if (real && g.part >= 0) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                   __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+          } else if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(o[8 * c + 2 * e]) * inv,
+                                 __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+              dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    } else {
+      // both chains hold a state of the same rows: exchange (m, l), then each group of warps
+      // writes half of the channels
+      mi.ml[t][r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mi.meet);
+      if (!tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status)) return;
+      if (!tc::wait_warp(&mi.o_full[0], no[0]++ & 1, &mi.quit, status)) return;
+      if (nt > 1 && !tc::wait_warp(&mi.o_full[1], no[1]++ & 1, &mi.quit, status)) return;
+      tc::fence_after();
+      if (any) {
+        const float2 s0 = mi.ml[0][r], s1 = mi.ml[1][r];
+        m = fmaxf(s0.x, s1.x);
+        const float f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
+        const float f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
+        l = s0.y * f0 + s1.y * f1;
+        const float inv = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int c0 = t * (D / 2); c0 < (t + 1) * (D / 2); c0 += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(tmem + lanes + 256 + c0, o);
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(o[c]) * f0;
+          if (nt > 1) {
+            tc::tmem_ld32(tmem + lanes + 256 + D + c0, o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(o[c]) * f1;
+          }
+          if (real && g.part >= 0) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          } else if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              dst[c] = make_uint4(pack_bf16(v[8 * c] * inv, v[8 * c + 1] * inv),
+                                  pack_bf16(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
+                                  pack_bf16(v[8 * c + 4] * inv, v[8 * c + 5] * inv),
+                                  pack_bf16(v[8 * c + 6] * inv, v[8 * c + 7] * inv));
+          }
+          __syncwarp();
+        }
+      }
+      // the other chain's accumulator and state may be overwritten once all have read them
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mi.meet);
+      if (!tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status)) return;
+    }
+    if (real && (!g.split || t == 0)) {
+      if (g.part >= 0)
+        a.part_ml[prow] = make_float2(m, l);
+      else
+        a.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const Args a) {
+  using Y = Lay<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = smem_u32(smem_raw);
+  Misc& mi = *reinterpret_cast<Misc*>(smem_raw + Y::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < Y::kStages; ++i) {
+      mbar_init(&mi.full[i], 1);
+      mbar_init(&mi.empty[i], 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&mi.seg_full[i], 1);
+      mbar_init(&mi.seg_empty[i], 9);  // the issuing thread and eight softmax warps
+    }
+    mbar_init(&mi.q_full, 1);
+    mbar_init(&mi.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&mi.s_full[t], 1);
+      mbar_init(&mi.p_full[t], 4);
+      mbar_init(&mi.o_full[t], 1);
+    }
+    mbar_init(&mi.meet, 8);
+    mbar_init(&mi.drain, 1);
+    mi.quit = 0;
+    fence_mbar_init();
+    // everything below reads what earlier kernels of the stream wrote
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  if (warp == 8) tc::tmem_alloc_all(&mi.tmem);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = mi.tmem;
+  if (warp < 8) {
+    soften<D>(a, smem, mi, tmem, warp >> 2);
+  } else if (warp == 8) {
+    if ((tid & 31) == 0) {
+      multiply<D>(a, smem, mi, tmem);
+      tc::commit(&mi.drain);
+      mbar_wait(&mi.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    produce<D>(a, smem, mi, &qmap, &kmap, &vmap);
+    __syncwarp();
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 8) tc::tmem_free_all(tmem);
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// Joins the pieces of the cut items: out = sum_p 2^(m_p - M) O_p / L, in piece order.  A row
+// is one warp's (SPLIT: a CTA's, whose eight warps take every eighth piece), a lane holds
+// D / 32 channels.  Also returns the item counter to zero for the next call.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ part_o,
+                                                   const float2* __restrict__ part_ml,
+                                                   const ChunkCut* __restrict__ cut,
+                                                   int32_t* ticket, uint16_t* __restrict__ out,
+                                                   float* __restrict__ lse, int rows_cap, int Hq,
+                                                   int G, int TB) {
+  constexpr int C = D / 32;
+  __shared__ float acc_s[8][D];
+  __shared__ float2 ml_s[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  if (c == 0 && blockIdx.y == 0 && threadIdx.x == 0) *ticket = 0;
+  const ChunkCut k = cut[c];
+  const int r = SPLIT ? blockIdx.y : blockIdx.y * 8 + warp;
+  const int tile = r >> 7, tok = (r & 127) / G, gh = (r & 127) % G, tk = tok + tile * TB;
+  if (k.nparts <= 0 || tok >= TB || tk >= k.ntok) return;  // per warp, or per CTA (SPLIT)
+  float M = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+  for (int e = 0; e < C; ++e) acc[e] = 0.f;
+  auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_cap + r; };
+  const int p0 = SPLIT ? warp : 0, step = SPLIT ? 8 : 1;
+  for (int p = p0 + lane * step; p < k.nparts; p += 32 * step) M = fmaxf(M, part_ml[slot(p)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+  for (int p = p0; p < k.nparts; p += step) {
+    const float2 ml = part_ml[slot(p)];
+    const float* src = part_o + slot(p) * D + lane * C;
+    float v[C];
+#pragma unroll
+    for (int e = 0; e < C; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(src + e);
+      v[e] = x.x;
+      v[e + 1] = x.y;
+    }
+    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    l += f * ml.y;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] += f * v[e];
+  }
+  if (SPLIT) {
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc_s[warp][lane * C + e] = acc[e];
+    if (lane == 0) ml_s[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp) return;
+    float W = -INFINITY;
+    for (int w = 0; w < 8; ++w) W = fmaxf(W, ml_s[w].x);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      const float2 ml = ml_s[w];
+      const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - W);
+      l += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < C; ++e) acc[e] += f * acc_s[w][lane * C + e];
+    }
+    M = W;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t orow = (size_t)(k.row0 + tk) * Hq + k.h * G + gh;
+#pragma unroll
+  for (int e = 0; e < C; e += 2)
+    *reinterpret_cast<uint32_t*>(out + orow * D + lane * C + e) =
+        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0)
+    lse[orow] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+static int rows_cap(const sa_geom& g, int n_tokens) {
+  const int G = g.Hq / g.Hkv, TB = 128 / G;
+  return n_tokens > TB ? 256 : (n_tokens > 0 ? n_tokens : 1) * G;
+}
+
+static cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem,
+                          cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+template <int D>
+static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream) {
+  using Y = Lay<D>;
+  Args a;
+  a.G = g.Hq / g.Hkv;
+  a.TB = 128 / a.G;
+  a.shape.cu_new = c.cu_new;
+  a.shape.seq_lens = c.seq_lens;
+  a.shape.n_tokens = c.n_tokens;
+  a.shape.B = g.B;
+  a.shape.H = g.Hkv;
+  a.shape.BT = 2 * a.TB;
+  a.shape.ST = a.TB;
+  const int longest = 1 << 30;  // no sequence is longer
+  a.shape.sink = c.sink < longest ? c.sink : longest;
+  a.shape.window = c.window < longest ? c.window : longest;
+  a.shape.cap = (int64_t)g.max_pages * g.P;
+  a.shape.status = c.status;
+  a.shape.ticket = c.ticket;
   a.page_table = c.page_table;
-  a.seq_lens = c.seq_lens;
   a.out = static_cast<uint16_t*>(c.out);
   a.lse = c.lse;
-  a.status = c.status;
-  a.n_tokens = c.n_tokens;
-  a.B = g.B;
+  a.rows_cap = rows_cap(g, c.n_tokens);
+  const size_t slots = 2 * (size_t)c.n_sm * a.rows_cap;
+  uint8_t* w = c.scratch;
+  a.cut = reinterpret_cast<ChunkCut*>(w);
+  w += up256(c.n_sm * sizeof(ChunkCut));
+  a.part_ml = reinterpret_cast<float2*>(w);
+  w += up256(slots * sizeof(float2));
+  a.part_o = reinterpret_cast<float*>(w);
   a.Hq = g.Hq;
   a.Hkv = g.Hkv;
   a.P = g.P;
+  a.page_shift = g.P == 16 ? 4 : g.P == 32 ? 5 : 6;
   a.max_pages = g.max_pages;
   a.n_pool = g.n_pool;
-  a.sink = c.sink;
-  a.window = c.window;
   a.scale_log2 = c.scale * 1.4426950408889634f;
-  const int64_t ctas = ((int64_t)c.n_tokens * g.Hq + 7) / 8;
-  if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  CUtensorMap qm, km, vm;
+  const uint64_t rows = (uint64_t)g.n_pool * g.Hkv * g.P;
+  if (!encode_heads_tmap(&qm, c.q, D, g.Hq, c.n_tokens, 64, a.G, a.TB) ||
+      !encode_rows_tmap(&km, c.k_cache, D, rows, 64, g.P) ||
+      !encode_rows_tmap(&vm, c.v_cache, D, rows, 64, g.P))
+    return cudaErrorInvalidValue;
+  const void* fn = reinterpret_cast<const void*>(attend_kernel<D>);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Y::kSmem);
+  if (e != cudaSuccess) return e;
+  void* args[] = {&qm, &km, &vm, &a};
+  if ((e = launch(fn, dim3(c.n_sm), kThreads, Y::kSmem, stream, args)) != cudaSuccess) return e;
+  const bool split = a.rows_cap <= 64;
+  const dim3 grid(c.n_sm, split ? a.rows_cap : (a.rows_cap + 7) / 8);
+  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut,      &a.shape.ticket, &a.out,
+                   &a.lse,    &a.rows_cap, &a.Hq, &a.G, &a.TB};
+  return launch(split ? reinterpret_cast<const void*>(join_kernel<D, true>)
+                      : reinterpret_cast<const void*>(join_kernel<D, false>),
+                grid, 256, 0, stream, jargs);
+}
+
+static size_t bytes(const sa_geom& g, int n_tokens, int n_sm) {
+  const size_t slots = 2 * (size_t)n_sm * rows_cap(g, n_tokens);
+  return up256(n_sm * sizeof(ChunkCut)) + up256(slots * sizeof(float2)) + slots * g.Dv * 4;
+}
+
+}  // namespace chunk
+
+size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm) {
+  return g.v_aliases_k ? 0 : chunk::bytes(g, n_tokens, n_sm);
+}
+
+cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream) {
   switch (g.Dk) {
-    case 64: attend_chunk_kernel<64, 64><<<(unsigned)ctas, 256, 0, stream>>>(a); break;
-    case 128: attend_chunk_kernel<128, 128><<<(unsigned)ctas, 256, 0, stream>>>(a); break;
-    case 576: attend_chunk_kernel<576, 512><<<(unsigned)ctas, 256, 0, stream>>>(a); break;
+    case 64: return chunk::run<64>(g, c, stream);
+    case 128: return chunk::run<128>(g, c, stream);
+    case 576: return launch_chunk_mla(g, c, stream);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace sa

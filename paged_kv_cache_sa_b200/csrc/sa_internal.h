@@ -168,14 +168,19 @@ struct ChunkCall {
   float* lse;
   uint8_t* scratch;  // workspace behind the header, chunk_workspace_bytes
   int32_t* status;
+  int32_t* ticket;  // header word, zero between calls: the next whole item to hand out
   int n_sm;
 };
 size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm);
 cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream);
+cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t stream);
 
 // TMA descriptor encoder from the driver (resolved once through the runtime).
 bool encode_rows_tmap(void* tmap_out, const void* base, uint64_t inner_elems, uint64_t rows,
                       uint32_t box_inner, uint32_t box_rows);
+bool encode_heads_tmap(void* tmap_out, const void* base, uint64_t inner, uint64_t heads,
+                       uint64_t tokens, uint32_t box_inner, uint32_t box_heads,
+                       uint32_t box_tokens);
 // 3-D descriptor of a [rows][128] bf16 pool: one box = box_rows rows, both 128-byte halves.
 bool encode_rows3_tmap(void* tmap_out, const void* base, uint64_t rows, uint32_t box_rows);
 
