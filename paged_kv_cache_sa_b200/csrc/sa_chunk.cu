@@ -622,26 +622,9 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ par
     lse[orow] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-static size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
 static int rows_cap(const sa_geom& g, int n_tokens) {
   const int G = g.Hq / g.Hkv, TB = 128 / G;
   return n_tokens > TB ? 256 : (n_tokens > 0 ? n_tokens : 1) * G;
-}
-
-static cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem,
-                          cudaStream_t stream, void** args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 template <int D>
@@ -655,6 +638,7 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   a.shape.n_tokens = c.n_tokens;
   a.shape.B = g.B;
   a.shape.H = g.Hkv;
+  a.shape.inner = 1;
   a.shape.BT = 2 * a.TB;
   a.shape.ST = a.TB;
   const int longest = 1 << 30;  // no sequence is longer
@@ -670,9 +654,9 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   const size_t slots = 2 * (size_t)c.n_sm * a.rows_cap;
   uint8_t* w = c.scratch;
   a.cut = reinterpret_cast<ChunkCut*>(w);
-  w += up256(c.n_sm * sizeof(ChunkCut));
+  w += chunk_up256(c.n_sm * sizeof(ChunkCut));
   a.part_ml = reinterpret_cast<float2*>(w);
-  w += up256(slots * sizeof(float2));
+  w += chunk_up256(slots * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(w);
   a.Hq = g.Hq;
   a.Hkv = g.Hkv;
@@ -692,25 +676,25 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
                                        (int)Y::kSmem);
   if (e != cudaSuccess) return e;
   void* args[] = {&qm, &km, &vm, &a};
-  if ((e = launch(fn, dim3(c.n_sm), kThreads, Y::kSmem, stream, args)) != cudaSuccess) return e;
+  if ((e = chunk_launch(fn, dim3(c.n_sm), kThreads, Y::kSmem, stream, args)) != cudaSuccess) return e;
   const bool split = a.rows_cap <= 64;
   const dim3 grid(c.n_sm, split ? a.rows_cap : (a.rows_cap + 7) / 8);
   void* jargs[] = {&a.part_o, &a.part_ml, &a.cut,      &a.shape.ticket, &a.out,
                    &a.lse,    &a.rows_cap, &a.Hq, &a.G, &a.TB};
-  return launch(split ? reinterpret_cast<const void*>(join_kernel<D, true>)
+  return chunk_launch(split ? reinterpret_cast<const void*>(join_kernel<D, true>)
                       : reinterpret_cast<const void*>(join_kernel<D, false>),
                 grid, 256, 0, stream, jargs);
 }
 
 static size_t bytes(const sa_geom& g, int n_tokens, int n_sm) {
   const size_t slots = 2 * (size_t)n_sm * rows_cap(g, n_tokens);
-  return up256(n_sm * sizeof(ChunkCut)) + up256(slots * sizeof(float2)) + slots * g.Dv * 4;
+  return chunk_up256(n_sm * sizeof(ChunkCut)) + chunk_up256(slots * sizeof(float2)) + slots * g.Dv * 4;
 }
 
 }  // namespace chunk
 
 size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm) {
-  return g.v_aliases_k ? 0 : chunk::bytes(g, n_tokens, n_sm);
+  return g.v_aliases_k ? chunk_mla_workspace_bytes(n_sm) : chunk::bytes(g, n_tokens, n_sm);
 }
 
 cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream) {

@@ -9,10 +9,12 @@
 //
 // Long lists are cut: the steps of all items, laid end to end in (sequence, head, block)
 // order, are dealt to the CTAs in equal runs, so a CTA holds at most two cut pieces (the end
-// of one item, the start of another), kept in workspace slots 2 c and 2 c + 1 and joined by a
-// second kernel.  When there are at least four times as many steps per CTA as the longest
+// of one item, the start of another), kept in workspace slots 2 c and 2 c + 1 of CTA c and
+// joined by a second kernel.  When there are at least four times as many steps per CTA as the longest
 // item has, nothing is cut: CTAs draw whole items from a counter, which keeps the CTAs on the
 // same head and so on the same keys in L2, longest blocks of a head first.
+// With inner > 1 the head groups of one piece go to `inner` neighbouring CTAs at the same time
+// instead of one after the other: they read the same keys.
 #pragma once
 
 #include "sa_common.cuh"
@@ -48,7 +50,8 @@ struct ChunkShape {
   const int32_t* cu_new;
   const int32_t* seq_lens;
   int n_tokens, B;
-  int H;           // head groups per token
+  int H;           // head groups per token, one after the other
+  int inner;       // head groups side by side: CTAs [inner w, inner w + inner) share run w
   int BT;          // tokens of a full block
   int ST;          // blocks of at most this many tokens walk two tiles a step
   int sink, window;
@@ -92,7 +95,8 @@ __device__ __forceinline__ bool chunk_seq(const ChunkShape& s, int b, int& c0, i
 // Every member function is called by one whole warp.
 struct ChunkSched {
   ChunkShape s;
-  int nc, c;             // CTAs that get work, this CTA
+  int nc, c;             // runs, and this CTA's
+  int lane_h;            // its head group (inner > 1)
   bool whole;
   int64_t total, left;   // steps of all items; of this CTA still to hand out
   int64_t pos;           // steps before the current item
@@ -146,7 +150,9 @@ struct ChunkSched {
 
   __device__ void init(const ChunkShape& shape, int cta, int n_cta) {
     s = shape;
-    c = cta;
+    c = cta / s.inner;
+    lane_h = cta % s.inner;
+    const int runs = n_cta / s.inner;
     const int lane = threadIdx.x & 31;
     total = 0;
     items = 0;
@@ -164,8 +170,8 @@ struct ChunkSched {
     }
     total *= s.H;
     items *= s.H;
-    nc = (int)min((int64_t)n_cta, total);
-    whole = total >= (int64_t)kWholeFactor * longest * n_cta;
+    nc = (int)min((int64_t)runs, total);
+    whole = total >= (int64_t)kWholeFactor * longest * runs;
     left = 0;
     if (total == 0) {
       whole = false;
@@ -237,8 +243,9 @@ struct ChunkSched {
     g.nparts = 0;
     g.part = -1;
     if (whole) {
-      const int t = __shfl_sync(0xffffffffu, ticket, 0);
-      if (t >= items || t < 0) return false;
+      const int drawn = __shfl_sync(0xffffffffu, ticket, 0), t = drawn / s.inner;
+      if (t >= items || drawn < 0) return false;
+      lane_h = drawn % s.inner;
       draw();
       for (;; gb += 32) {
         int nn, LL;
@@ -273,9 +280,9 @@ struct ChunkSched {
     const int end = off + take;
     fill(g, k, k.split ? 2 * off : off, k.split ? min(k.tiles, 2 * end) : end);
     if (off > 0) {
-      g.part = 2 * c;
+      g.part = 2 * (c * s.inner + lane_h);
     } else if (end < k.steps) {
-      g.part = 2 * c + 1;
+      g.part = 2 * (c * s.inner + lane_h) + 1;
       // CTAs whose runs start before the item's end: run r starts at floor(r total / nc)
       const int64_t e = pos + k.steps;
       const int last = (int)min((int64_t)nc - 1, (e * nc + total - 1) / total - 1);
@@ -304,7 +311,7 @@ struct ChunkSched {
     g.row0 = c0 + k.t0;
     g.ntok = k.nt;
     g.b = b;
-    g.h = h;
+    g.h = h * s.inner + lane_h;
     g.s0 = L - n + k.t0;
     g.L = L;
     g.na = k.na;
@@ -314,5 +321,23 @@ struct ChunkSched {
     g.split = k.split;
   }
 };
+
+inline size_t chunk_up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// A launch that may begin before the stream's previous kernel has ended (the kernels wait).
+inline cudaError_t chunk_launch(const void* fn, dim3 grid, int threads, size_t smem,
+                                cudaStream_t stream, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
 
 }  // namespace sa

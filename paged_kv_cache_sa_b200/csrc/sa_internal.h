@@ -173,6 +173,7 @@ struct ChunkCall {
 };
 size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm);
 cudaError_t launch_chunk(const sa_geom& g, const ChunkCall& c, cudaStream_t stream);
+size_t chunk_mla_workspace_bytes(int n_sm);
 cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t stream);
 
 // TMA descriptor encoder from the driver (resolved once through the runtime).
