@@ -9,14 +9,19 @@
 // once, 2^-25 turns) goes to sincospif.  The rotation is fp32; the only rounding to bf16 is
 // the store.
 //
-// One CTA per (sequence, page that receives tokens): the page is the unit that has a single
-// owner, so the summaries (min/max over all valid rows of the page, the old ones read back
-// from the cache, the new ones still in registers) need no atomics and no second launch.
-// cos/sin of the page's new tokens are computed once into shared memory and serve every query
-// and key head.  A lane holds a "unit": two 16-byte chunks of one row that rotate together
-// (j and j + rot/2 in the half-split form, neighbours in the interleaved form), so loads and
-// stores stay 16 bytes wide and coalesced.  Bound by HBM: every row is read once and written
-// once.
+// Two kinds of CTA in one launch:
+//   pages: one CTA per (sequence, page that receives tokens).  The page is the unit that has a
+//     single owner, so the summaries (min/max over all valid rows of the page, the old ones
+//     read back from the cache, the new ones still in registers) need no atomics and no second
+//     launch.  A warp takes a KV head (latent rows: the CTA's row groups share the page).
+//   tokens: a run of rows of the call, as many as make about 1024 units; rotates their queries
+//     and copies their values.  Queries are most of the bytes (all of them in the latent
+//     geometry: 147 KB a token), so they are spread over the grid whatever the pages are, and
+//     their loads are in flight before the sequence and page of the rows are known.
+// cos/sin are computed once per CTA into shared memory and serve every head.  A lane holds a
+// "unit": two 16-byte chunks of one row that rotate together (j and j + rot/2 in the
+// half-split form, neighbours in the interleaved form), so loads and stores stay 16 bytes wide
+// and coalesced.  Bound by HBM: every row is read once and written once.
 #include "sa_common.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.h"
@@ -27,6 +32,8 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kMaxRun = 64;     // tokens of a token CTA, at most
+constexpr int kRunUnits = 1024; // query units that a token CTA is sized for
 
 struct AppendArgs {
   const uint4* q;
@@ -46,6 +53,9 @@ struct AppendArgs {
   int n_tokens, B, Hq, Hkv, P, max_pages, n_pool;
   int rot_start, rot_dim, interleaved;
   int want;  // 0: no summaries, 1: bf16 rows, 2: fp8 records
+  int n_page_ctas, run;    // CTAs of the first kind; tokens of a CTA of the second
+  uint32_t per_q, per_v;   // units of a token's queries, chunks of its values
+  uint32_t inv_q, inv_v;   // ceil(2^32 / per): e / per = mulhi(e, inv) while e * per < 2^32
 };
 
 // the two chunks of unit u of a row, and its first rotation pair (-1: not rotated)
@@ -148,11 +158,19 @@ __device__ __forceinline__ void new_tokens(const int32_t* cu, const int32_t* len
   if (!ok) report(status, SA_ERR_DEVICE_CHECK);
 }
 
+// cos and sin of half a turn's multiples: angle pos * f as a number of turns in fp64
+__device__ __forceinline__ float2 cos_sin(int pos, float f) {
+  const double turns = (double)pos * (double)f * 0.15915494309189535;
+  const float frac = (float)(2.0 * (turns - rint(turns)));  // half turns in [-1, 1]
+  float sn, co;
+  sincospif(frac, &sn, &co);
+  return make_float2(co, sn);
+}
+
 // CPR = 16-byte chunks per key row (Dk / 8).
 template <int CPR>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+__device__ __forceinline__ void append_pages(const AppendArgs& a, float2* cs) {
   constexpr int U = CPR / 2;  // units per row
-  extern __shared__ float2 cs[];  // [new tokens of the page][rot_dim / 2]
   __shared__ int scan[kAppendWarps];
   __shared__ int found[2];  // sequence and page of this CTA's item
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -160,7 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const bool inter = a.interleaved != 0;
   const int64_t cap = (int64_t)a.max_pages * a.P;
 
-  for (int item = blockIdx.x;; item += gridDim.x) {
+  for (int item = blockIdx.x;; item += a.n_page_ctas) {
     // ---- the item's sequence and page: running count of touched pages over the batch
     if (tid == 0) found[0] = -1;
     int before = 0;
@@ -217,11 +235,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     // ---- cos and sin of every (new token, pair)
     for (int e = tid; e < cnt * half; e += kAppendThreads) {
       const int i = e / half, j = e - i * half;
-      const double turns = (double)(pos0 + i) * (double)a.inv_freq[j] * 0.15915494309189535;
-      const float frac = (float)(2.0 * (turns - rint(turns)));  // half turns in [-1, 1]
-      float sn, co;
-      sincospif(frac, &sn, &co);
-      cs[e] = make_float2(co, sn);
+      cs[e] = cos_sin(pos0 + i, a.inv_freq[j]);
     }
     __syncthreads();
 
@@ -232,8 +246,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       const int u = lane % U, rg = lane / U;
       constexpr int RPW = 32 / U;
       const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
-      for (int h = blockIdx.y * kAppendWarps + warp; h < a.Hkv;
-           h += gridDim.y * kAppendWarps) {
+      for (int h = warp; h < a.Hkv; h += kAppendWarps) {
         uint4* blk = a.k_cache + ((size_t)phys * a.Hkv + h) * a.P * CPR;
         Range ra, rb;
         ra.clear();
@@ -294,10 +307,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
           }
         }
       }
-    } else if (blockIdx.y == 0) {
+    } else {
       // latent rows (one KV head): the CTA's row groups split the page's rows, their
       // partial ranges meet in shared memory
-      constexpr int NG = kAppendThreads / U;
+      constexpr int NG = kAppendThreads / U - 1;  // (shared memory: one group of threads rests)
       __shared__ Range part[NG][CPR];
       const int u = tid % U, rg = tid / U;
       const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
@@ -341,35 +354,107 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       }
     }
 
-    // ---- queries: (token, head) rows of the page's new tokens, all threads of the column
-    const int first = blockIdx.y * kAppendThreads + tid, step = gridDim.y * kAppendThreads;
-    if (a.q) {
-      const int n_e = cnt * a.Hq * U;
-#pragma unroll 4
-      for (int e = first; e < n_e; e += step) {
-        const int row = e / U, u = e % U;
-        const int i = row / a.Hq, h = row - i * a.Hq;
-        const Unit x = unit_of(u, a.rot_start, a.rot_dim, inter);
-        const uint4* src = a.q + (size_t)(row0 + i) * a.q_stride + h * CPR;
-        uint4 va = src[x.ca], vb = src[x.cb];
-        if (x.pair >= 0) rotate_unit(va, vb, cs + i * half + x.pair, inter);
-        uint4* dst = a.q_out + ((size_t)(row0 + i) * a.Hq + h) * CPR;
-        dst[x.ca] = va;
-        dst[x.cb] = vb;
+    __syncthreads();  // cs[], found[] and part[] are free for the next item
+  }
+}
+
+// Tokens [r0, r0 + run) of the call: queries rotated, values to their slots.
+template <int CPR>
+__device__ __forceinline__ void append_tokens(const AppendArgs& a, float2* cs, int r0) {
+  constexpr int U = CPR / 2;
+  __shared__ int t_seq[kMaxRun], t_slot[kMaxRun], t_pos[kMaxRun], t_row[kMaxRun];
+  const int tid = threadIdx.x;
+  const int half = a.rot_dim >> 1;
+  const bool inter = a.interleaved != 0;
+  const int64_t cap = (int64_t)a.max_pages * a.P;
+  const int cnt = min(a.run, a.n_tokens - r0);
+  // queries of four units per thread at a time; the first four's loads start here
+  const uint32_t n_q = a.q ? cnt * a.per_q : 0;
+  uint4 va[4], vb[4];
+  auto fetch = [&](uint32_t e0) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t e = e0 + x * kAppendThreads;
+      if (e < n_q) {
+        const uint32_t i = a.per_q == 1 ? e : __umulhi(e, a.inv_q), w = e - i * a.per_q;
+        const Unit y = unit_of(w % U, a.rot_start, a.rot_dim, inter);
+        const uint4* src = a.q + (size_t)(r0 + i) * a.q_stride + w / U * CPR;
+        va[x] = src[y.ca];
+        vb[x] = src[y.cb];
       }
     }
-    // ---- values: plain rows into their slots
-    if (a.v) {
-      const int n_e = a.Hkv * cnt * CPR;
-#pragma unroll 4
-      for (int e = first; e < n_e; e += step) {
-        const int row = e / CPR, c = e % CPR;
-        const int h = row / cnt, i = row - h * cnt;
-        a.v_cache[(((size_t)phys * a.Hkv + h) * a.P + slot0 + i) * CPR + c] =
-            a.v[(size_t)(row0 + i) * a.v_stride + h * CPR + c];
+  };
+  fetch(tid);
+  if (tid < kMaxRun) t_row[tid] = -1;
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kAppendThreads) {
+    int c0, n, L;
+    new_tokens(a.cu_new, a.seq_lens, b, a.n_tokens, cap, a.status, c0, n, L);
+    const int i0 = max(c0, r0), i1 = min(c0 + n, r0 + cnt);
+    if (i0 < i1) {
+      const int pos = (a.logical_lens ? a.logical_lens[b] : L) - n - c0;
+      for (int i = i0; i < i1; ++i) {
+        t_seq[i - r0] = b;
+        t_slot[i - r0] = L - n + i - c0;
+        t_pos[i - r0] = pos + i;
+        t_row[i - r0] = 0;
       }
     }
-    __syncthreads();  // cs[] and found[] are free for the next item
+  }
+  __syncthreads();
+  // row of the token in the pool (page * P + slot), -1: belongs to no sequence or no page
+  if (tid < cnt && t_row[tid] == 0) {
+    const int lp = t_slot[tid] / a.P;
+    const int phys = a.page_table[(size_t)t_seq[tid] * a.max_pages + lp];
+    const bool ok = phys >= 0 && phys < a.n_pool;
+    if (!ok) report(a.status, SA_ERR_DEVICE_CHECK);
+    t_row[tid] = ok ? phys : -1;
+    t_slot[tid] -= lp * a.P;
+  }
+  for (int e = tid; e < (a.q ? cnt * half : 0); e += kAppendThreads) {
+    const int i = e / half;
+    cs[e] = cos_sin(t_pos[i], a.inv_freq[e - i * half]);
+  }
+  __syncthreads();
+  for (uint32_t e0 = tid; e0 < n_q; e0 += 4 * kAppendThreads) {
+    if (e0 != tid) fetch(e0);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t e = e0 + x * kAppendThreads;
+      const uint32_t i = a.per_q == 1 ? e : __umulhi(e, a.inv_q), w = e - i * a.per_q;
+      if (e < n_q && t_row[i] >= 0) {
+        const Unit y = unit_of(w % U, a.rot_start, a.rot_dim, inter);
+        if (y.pair >= 0) rotate_unit(va[x], vb[x], cs + i * half + y.pair, inter);
+        uint4* dst = a.q_out + ((size_t)(r0 + i) * a.Hq + w / U) * CPR;
+        dst[y.ca] = va[x];
+        dst[y.cb] = vb[x];
+      }
+    }
+  }
+  const uint32_t n_v = a.v ? cnt * a.per_v : 0;
+#pragma unroll 4
+  for (uint32_t e = tid; e < n_v; e += kAppendThreads) {
+    const uint32_t i = a.per_v == 1 ? e : __umulhi(e, a.inv_v), w = e - i * a.per_v;
+    const int phys = t_row[i];
+    const uint4 x = a.v[(size_t)(r0 + i) * a.v_stride + w];
+    if (phys >= 0)
+      a.v_cache[(((size_t)phys * a.Hkv + w / CPR) * a.P + t_slot[i]) * CPR + w % CPR] = x;
+  }
+  __syncthreads();  // the shared arrays are free for the next run
+}
+
+template <int CPR>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a) {
+  extern __shared__ float2 cs[];  // [tokens][rot_dim / 2]
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x < a.n_page_ctas) {
+    append_pages<CPR>(a, cs);
+  } else {
+    const int64_t step = (int64_t)(gridDim.x - a.n_page_ctas) * a.run;
+    for (int64_t r0 = (int64_t)(blockIdx.x - a.n_page_ctas) * a.run; r0 < a.n_tokens; r0 += step)
+      append_tokens<CPR>(a, cs, (int)r0);
   }
 }
 
@@ -409,17 +494,37 @@ cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t st
   const int64_t nseq = g.B < c.n_tokens ? g.B : c.n_tokens;
   int64_t items = c.n_tokens / g.P + 2 * nseq;
   if (items > c.n_tokens) items = c.n_tokens;
-  if (items > 65535) items = 65535;  // the kernel strides over the rest
-  const int split = items >= 296 ? 1 : items >= 148 ? 2 : 4;
-  const dim3 grid((unsigned)items, split), block(kAppendThreads);
-  const size_t smem = (size_t)g.P * (c.rot_dim / 2) * sizeof(float2);  // at most 32 KB
+  if (items > 1 << 20) items = 1 << 20;  // the kernel strides over the rest
+  a.n_page_ctas = (int)items;
+  a.per_q = g.Hq * (g.Dk / 16);
+  a.per_v = g.Hkv * (g.Dv / 8);
+  a.inv_q = (uint32_t)(((1ull << 32) + a.per_q - 1) / a.per_q);
+  a.inv_v = (uint32_t)(((1ull << 32) + a.per_v - 1) / a.per_v);
+  a.run = kRunUnits / (int)a.per_q;
+  a.run = a.run < 1 ? 1 : a.run > kMaxRun ? kMaxRun : a.run;
+  int64_t runs = a.q || a.v ? ((int64_t)c.n_tokens + a.run - 1) / a.run : 0;
+  if (runs > 1 << 20) runs = 1 << 20;
+  // cos and sin of a page's or a run's tokens: at most 32 KB
+  const size_t smem = (size_t)(g.P > a.run ? g.P : a.run) * (c.rot_dim / 2) * sizeof(float2);
+  const void* fn;
   switch (g.Dk) {
-    case 64: append_kernel<8><<<grid, block, smem, stream>>>(a); break;
-    case 128: append_kernel<16><<<grid, block, smem, stream>>>(a); break;
-    case 576: append_kernel<72><<<grid, block, smem, stream>>>(a); break;
+    case 64: fn = reinterpret_cast<const void*>(append_kernel<8>); break;
+    case 128: fn = reinterpret_cast<const void*>(append_kernel<16>); break;
+    case 576: fn = reinterpret_cast<const void*>(append_kernel<72>); break;
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items + runs));
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // may begin before the previous kernel has ended (it waits)
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {&a};
+  return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace sa
