@@ -179,7 +179,7 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
   }
 }
 
-// ---- one thread issues every product ----------------------------------------------------
+// ---- one warp issues every product ----------------------------------------------------
 template <int D>
 __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem) {
   using Y = Lay<D>;
@@ -188,10 +188,12 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
   int32_t* status = a.shape.status;
   int it = 0, np[2] = {0, 0};
   auto staged = [&](int x) {
-    const bool r = tc::wait(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status);
+    const bool r =
+        tc::wait_warp(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status);
     tc::fence_after();
     return r;
   };
+  // (the rest runs in one lane)
   auto scores = [&](int qt, int t, int x) {  // S_t = Q_qt K^T of stage x
     const uint32_t q = smem + Y::kQ + qt * Y::kTileBytes;
     const uint32_t k = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
@@ -202,73 +204,95 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
     }
     tc::commit(&mi.s_full[t]);
   };
-  auto values = [&](int t, int x, bool first) -> bool {  // O_t += P_t V of stage x
-    const bool r = tc::wait(&mi.p_full[t], np[t]++ & 1, &mi.quit, status);
-    tc::fence_after();
-    if (!r) return false;
+  auto values = [&](int t, int x, bool first) {  // O_t += P_t V of stage x
     const uint32_t v = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
 #pragma unroll
     for (int kk = 0; kk < kKeyTile / 16; ++kk)
       tc::mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8,
                  tc::desc(v + kk * 2048, kHalfBytes), id_o, !(first && kk == 0));
-    return true;
+  };
+  auto probs = [&](int t) {  // P_t is there
+    const bool r = tc::wait_warp(&mi.p_full[t], np[t]++ & 1, &mi.quit, status);
+    tc::fence_after();
+    return r;
   };
   for (int n = 0;; ++n) {
     const int slot = n % kSegs;
-    if (!tc::wait(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
-    const bool valid = mi.seg[slot].valid != 0, split = mi.seg[slot].split != 0;
-    const int nt = mi.seg[slot].i1 - mi.seg[slot].i0;
-    mbar_arrive(&mi.seg_empty[slot]);
+    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
+    const int nt = __shfl_sync(0xffffffffu, mi.seg[slot].i1 - mi.seg[slot].i0, 0);
+    const bool valid = __shfl_sync(0xffffffffu, mi.seg[slot].valid, 0) != 0;
+    const bool split = __shfl_sync(0xffffffffu, mi.seg[slot].split, 0) != 0;
+    if (tc::elect()) mbar_arrive(&mi.seg_empty[slot]);
     if (!valid) return;
-    if (!tc::wait(&mi.q_full, n & 1, &mi.quit, status)) return;
+    if (!tc::wait_warp(&mi.q_full, n & 1, &mi.quit, status)) return;
     if (!split) {
       int k = it++;
       if (!staged(k)) return;
-      scores(0, 0, k);
-      scores(1, 1, k);
-      tc::commit(&mi.empty[k % Y::kStages]);
-      if (nt == 1) tc::commit(&mi.q_empty);
+      if (tc::elect()) {
+        scores(0, 0, k);
+        scores(1, 1, k);
+        tc::commit(&mi.empty[k % Y::kStages]);
+        if (nt == 1) tc::commit(&mi.q_empty);
+      }
+      __syncwarp();
       for (int i = 0; i < nt; ++i) {
         const int v = it++;
         const bool more = i + 1 < nt;
-        if (!staged(v) || !values(0, v, i == 0)) return;
+        if (more) k = it++;
+        if (!staged(v) || !probs(0)) return;
+        if (tc::elect()) {
+          values(0, v, i == 0);
+          if (!more) tc::commit(&mi.o_full[0]);
+        }
+        __syncwarp();
         if (more) {
-          k = it++;
           if (!staged(k)) return;
-          scores(0, 0, k);
-        } else {
-          tc::commit(&mi.o_full[0]);
+          if (tc::elect()) scores(0, 0, k);
+          __syncwarp();
         }
-        if (!values(1, v, i == 0)) return;
-        tc::commit(&mi.empty[v % Y::kStages]);
-        if (more) {
-          scores(1, 1, k);
-          tc::commit(&mi.empty[k % Y::kStages]);
-          if (i + 2 == nt) tc::commit(&mi.q_empty);
-        } else {
-          tc::commit(&mi.o_full[1]);
+        if (!probs(1)) return;
+        if (tc::elect()) {
+          values(1, v, i == 0);
+          tc::commit(&mi.empty[v % Y::kStages]);
+          if (more) {
+            scores(1, 1, k);
+            tc::commit(&mi.empty[k % Y::kStages]);
+            if (i + 2 == nt) tc::commit(&mi.q_empty);
+          } else {
+            tc::commit(&mi.o_full[1]);
+          }
         }
+        __syncwarp();
       }
     } else {
       for (int i = 0; i < min(nt, 2); ++i) {
         const int k = it++;
         if (!staged(k)) return;
-        scores(0, i, k);
-        tc::commit(&mi.empty[k % Y::kStages]);
-        if (i + 1 == nt) tc::commit(&mi.q_empty);
+        if (tc::elect()) {
+          scores(0, i, k);
+          tc::commit(&mi.empty[k % Y::kStages]);
+          if (i + 1 == nt) tc::commit(&mi.q_empty);
+        }
+        __syncwarp();
       }
       for (int i = 0; i < nt; ++i) {
         const int t = i & 1, v = it++;
-        if (!staged(v) || !values(t, v, i < 2)) return;
-        tc::commit(&mi.empty[v % Y::kStages]);
+        if (!staged(v) || !probs(t)) return;
+        if (tc::elect()) {
+          values(t, v, i < 2);
+          tc::commit(&mi.empty[v % Y::kStages]);
+          if (i + 2 >= nt) tc::commit(&mi.o_full[t]);
+        }
+        __syncwarp();
         if (i + 2 < nt) {
           const int k = it++;
           if (!staged(k)) return;
-          scores(0, t, k);
-          tc::commit(&mi.empty[k % Y::kStages]);
-          if (i + 3 == nt) tc::commit(&mi.q_empty);
-        } else {
-          tc::commit(&mi.o_full[t]);
+          if (tc::elect()) {
+            scores(0, t, k);
+            tc::commit(&mi.empty[k % Y::kStages]);
+            if (i + 3 == nt) tc::commit(&mi.q_empty);
+          }
+          __syncwarp();
         }
       }
     }
@@ -531,8 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 8) {
     soften<D>(a, smem, mi, tmem, warp >> 2);
   } else if (warp == 8) {
-    if ((tid & 31) == 0) {
-      multiply<D>(a, smem, mi, tmem);
+    multiply<D>(a, smem, mi, tmem);
+    __syncwarp();
+    if (tc::elect()) {
       tc::commit(&mi.drain);
       mbar_wait(&mi.drain, 0);
     }

@@ -176,39 +176,47 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
   int it = 0;
   for (int n = 0;; ++n) {
     const int slot = n % kSegs;
-    if (!tc::wait(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
-    const bool valid = mi.seg[slot].valid != 0;
-    const int nt = mi.seg[slot].i1 - mi.seg[slot].i0;
-    mbar_arrive(&mi.seg_empty[slot]);
+    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
+    const int nt = __shfl_sync(0xffffffffu, mi.seg[slot].i1 - mi.seg[slot].i0, 0);
+    const bool valid = __shfl_sync(0xffffffffu, mi.seg[slot].valid, 0) != 0;
+    if (tc::elect()) mbar_arrive(&mi.seg_empty[slot]);
     if (!valid) return;
-    if (!tc::wait(&mi.q_full, n & 1, &mi.quit, status)) return;
+    if (!tc::wait_warp(&mi.q_full, n & 1, &mi.quit, status)) return;
     for (int i = 0; i < nt; ++i, ++it) {
 #pragma unroll
       for (int gr = 0; gr < kGroups; ++gr) {
-        if (!tc::wait(&mi.full[gr], it & 1, &mi.quit, status)) return;
+        if (!tc::wait_warp(&mi.full[gr], it & 1, &mi.quit, status)) return;
         tc::fence_after();
+        if (tc::elect()) {
 #pragma unroll
-        for (int kk = 0; kk < (gr == 4 ? 4 : 8); ++kk) {
-          const int sl = 2 * gr + (kk >> 2);
-          tc::mma_ss(tmem, tc::desc(smem + kKeys + sl * kSlice + (kk & 3) * 32),
-                     tc::desc(smem + sl * kQSlice + (kk & 3) * 32), id_s, gr + kk != 0);
+          for (int kk = 0; kk < (gr == 4 ? 4 : 8); ++kk) {
+            const int sl = 2 * gr + (kk >> 2);
+            tc::mma_ss(tmem, tc::desc(smem + kKeys + sl * kSlice + (kk & 3) * 32),
+                       tc::desc(smem + sl * kQSlice + (kk & 3) * 32), id_s, gr + kk != 0);
+          }
+          if (gr == 4) {
+            tc::commit(&mi.s_full);
+            if (i + 1 == nt) tc::commit(&mi.q_empty);
+          }
         }
+        __syncwarp();
       }
-      tc::commit(&mi.s_full);
-      if (i + 1 == nt) tc::commit(&mi.q_empty);
-      if (!tc::wait(&mi.p_full, it & 1, &mi.quit, status)) return;
+      if (!tc::wait_warp(&mi.p_full, it & 1, &mi.quit, status)) return;
       tc::fence_after();
+      if (tc::elect()) {
 #pragma unroll
-      for (int cb = 0; cb < 4; ++cb) {
+        for (int cb = 0; cb < 4; ++cb) {
 #pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)
-          tc::mma_ss(tmem + kO + cb * 64,
-                     tc::desc(smem + kKeys + 2 * cb * kSlice + kk * 2048, kSlice),
-                     tc::desc(smem + kP + kk * 2048), id_o, !(i == 0 && kk == 0));
-        tc::commit(&mi.empty[cb]);
+          for (int kk = 0; kk < kKeyTile / 16; ++kk)
+            tc::mma_ss(tmem + kO + cb * 64,
+                       tc::desc(smem + kKeys + 2 * cb * kSlice + kk * 2048, kSlice),
+                       tc::desc(smem + kP + kk * 2048), id_o, !(i == 0 && kk == 0));
+          tc::commit(&mi.empty[cb]);
+        }
+        tc::commit(&mi.empty[4]);
+        if (i + 1 == nt) tc::commit(&mi.o_full);
       }
-      tc::commit(&mi.empty[4]);
-      if (i + 1 == nt) tc::commit(&mi.o_full);
+      __syncwarp();
     }
   }
 }
@@ -276,30 +284,62 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
       }
       const bool seen = key <= s && (a.shape.window == 0 || key > s - a.shape.window ||
                                      key < a.shape.sink);
-      uint32_t x[32];
-      tc::tmem_ld32(tmem + lanes + 32 * t, x);
-      float top = -INFINITY;
+      // P with the maximum in use, in place of the scores, while the vote on it goes round
+      float p[32];
+      auto probabilities = [&](bool vote) {
+        uint32_t x[32];
+        tc::tmem_ld32(tmem + lanes + 32 * t, x);
+        float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 off = *reinterpret_cast<const float4*>(&mi.off[t][c]);
-        top = fmaxf(top, fmaf(__uint_as_float(x[c]), a.scale_log2, off.x));
-        top = fmaxf(top, fmaf(__uint_as_float(x[c + 1]), a.scale_log2, off.y));
-        top = fmaxf(top, fmaf(__uint_as_float(x[c + 2]), a.scale_log2, off.z));
-        top = fmaxf(top, fmaf(__uint_as_float(x[c + 3]), a.scale_log2, off.w));
-      }
-      const bool over = __any_sync(0xffffffffu, seen && (none || top > 8.f));
-      // round it: raise flag it % 3; flag (it + 1) % 3 was last read before the previous vote
-      if (lane == 0) {
-        if (wq == 0) *(volatile int*)&mi.vote[t][(it + 1) % 3] = 0;
-        if (over) *(volatile int*)&mi.vote[t][it % 3] = 1;
-      }
-      if (!meet()) return;
+        for (int c = 0; c < 32; c += 4) {
+          const float4 off = *reinterpret_cast<const float4*>(&mi.off[t][c]);
+          p[c] = fmaf(__uint_as_float(x[c]), a.scale_log2, off.x);
+          p[c + 1] = fmaf(__uint_as_float(x[c + 1]), a.scale_log2, off.y);
+          p[c + 2] = fmaf(__uint_as_float(x[c + 2]), a.scale_log2, off.z);
+          p[c + 3] = fmaf(__uint_as_float(x[c + 3]), a.scale_log2, off.w);
+        }
+        if (vote) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(p[c], p[c + 1]));
+          const bool over = __any_sync(0xffffffffu, seen && (none || top > 8.f));
+          // round it: raise flag it % 3; flag (it + 1) % 3 was last read before the last vote
+          if (lane == 0) {
+            if (wq == 0) *(volatile int*)&mi.vote[t][(it + 1) % 3] = 0;
+            if (over) *(volatile int*)&mi.vote[t][it % 3] = 1;
+            mbar_arrive(&mi.meet[t]);
+          }
+        }
+        const uint32_t prow = smem + kP + r * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 8 * u + 2 * e;
+            p[c] = seen ? fast_exp2(p[c]) : 0.f;
+            p[c + 1] = seen ? fast_exp2(p[c + 1]) : 0.f;
+            w[e] = pack_bf16(p[c], p[c + 1]);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           prow + (((4 * t + u) ^ (r & 7)) << 4)),
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      };
+      probabilities(true);
+      tc::fence_async_smem();
+      if (!tc::wait_warp(&mi.meet[t], nmeet++ & 1, &mi.quit, status)) return;
       if (*(volatile int*)&mi.vote[t][it % 3]) {
-        float v[32];
+        // raise the maximum: columns' maxima over the tile's keys, O^T and the sums rescaled
+        {
+          uint32_t x[32];
+          tc::tmem_ld32(tmem + lanes + 32 * t, x);
+          float v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          v[c] = seen ? __uint_as_float(x[c]) * a.scale_log2 : -INFINITY;
-        mi.red[t][wq][lane] = across<true>(v);
+          for (int c = 0; c < 32; ++c)
+            v[c] = seen ? __uint_as_float(x[c]) * a.scale_log2 : -INFINITY;
+          mi.red[t][wq][lane] = across<true>(v);
+        }
         if (!meet()) return;
         const float up = fmaxf(fmaxf(fmaxf(mi.red[t][0][lane], mi.red[t][1][lane]),
                                      fmaxf(mi.red[t][2][lane], mi.red[t][3][lane])),
@@ -326,32 +366,14 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
           tc::tmem_wait_st();
         }
         none = false;
+        probabilities(false);
+        tc::fence_async_smem();
       }
-      const uint32_t prow = smem + kP + r * 128;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = 8 * u + 2 * e;
-          const float2 off = *reinterpret_cast<const float2*>(&mi.off[t][c]);
-          const float p0 =
-              seen ? fast_exp2(fmaf(__uint_as_float(x[c]), a.scale_log2, off.x)) : 0.f;
-          const float p1 =
-              seen ? fast_exp2(fmaf(__uint_as_float(x[c + 1]), a.scale_log2, off.y)) : 0.f;
-          l[c] += p0;
-          l[c + 1] += p1;
-          w[e] = pack_bf16(p0, p1);
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         prow + (((4 * t + u) ^ (r & 7)) << 4)),
-                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
-      }
-      tc::fence_async_smem();
       tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&mi.p_full);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] += p[c];
     }
     // ---- results
     const float part = across<false>(l);
@@ -437,8 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 8) {
     soften(a, smem, mi, tmem, warp >> 2);
   } else if (warp == 8) {
-    if ((tid & 31) == 0) {
-      multiply(a, smem, mi, tmem);
+    multiply(a, smem, mi, tmem);
+    __syncwarp();
+    if (tc::elect()) {
       tc::commit(&mi.drain);
       mbar_wait(&mi.drain, 0);
     }

@@ -17,6 +17,19 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  Products and commits are issued under this test in
+// code that the whole warp runs: the descriptors then stay in uniform registers.  (One thread
+// branching off on its own lane number cost 64 cycles per product, whatever its shape.)
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // All 512 columns of the SM's tensor memory (one whole warp); address to `slot`.
 __device__ __forceinline__ void tmem_alloc_all(uint32_t* slot) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
