@@ -22,7 +22,8 @@
 // The maximum in use is only raised when a row's new maximum exceeds it by more than 2^8
 // (P then stays below 2^8, exact in range for bf16 and fp32): O is rescaled a few times per
 // row instead of at every tile, by the softmax warps themselves.
-// Warps 0-3 and 4-7: softmax of chain 0 and 1; 8: issues the products; 9: work list and TMA.
+// Warps 0-3 and 4-7: softmax of chain 0 and 1; 8: issues the products; 9: work list, queries
+// and K; 10: V (one warp for both had the copies of 16-token pages queue behind one another).
 #include "sa_chunk.cuh"
 #include "sa_internal.h"
 #include "sa_tc.cuh"
@@ -31,7 +32,9 @@ namespace sa {
 
 namespace chunk {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// registers: 168 a thread at launch (384 x 168 = 64512); 256 x 208 + 128 x 88 = 64512
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kSegs = 2;
 constexpr uint32_t kHalfBytes = kKeyTile * 128;  // 128 rows of 64 channels
 
@@ -51,7 +54,7 @@ struct Misc {
   ChunkSeg seg[kSegs];
   uint64_t full[10], empty[10];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], meet, drain;
+  uint64_t q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], meet, drain;
   uint32_t tmem;
   int quit;
 };
@@ -74,28 +77,99 @@ __device__ __forceinline__ int tile_of(const ChunkSeg& g, int i) {
   return i < g.na ? i : i - g.na + g.bs;
 }
 
-// ---- the producer warp: work list, queries and the ring of K and V tiles ---------------
+// Position in the ring, counted from the piece's first stage, of K and V of its i-th tile: K of
+// the first tile (two, if a step takes two), then V of a tile and K of the next without one.
+__device__ __forceinline__ int k_pos(bool split, int i) {
+  return split ? (i == 0 ? 0 : 2 * i - 1) : 2 * i;
+}
+__device__ __forceinline__ int v_pos(bool split, int nt, int i) {
+  return split && i + 1 < nt ? 2 * i + 2 : 2 * i + 1;
+}
+
+// ---- the producer warps: one makes the work list and loads queries and K, one loads V ----
 template <int D>
-__device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
-                                        const CUtensorMap* qmap, const CUtensorMap* kmap,
-                                        const CUtensorMap* vmap) {
+struct Loader {
   using Y = Lay<D>;
-  const int lane = threadIdx.x & 31;
+  const Args& a;
+  uint32_t smem;
+  Misc& mi;
+  const CUtensorMap* map;
+  int lane, ppt, my_page, my_half;
+
+  __device__ __forceinline__ Loader(const Args& args, uint32_t s, Misc& m, const CUtensorMap* mp)
+      : a(args), smem(s), mi(m), map(mp) {
+    lane = threadIdx.x & 31;
+    ppt = kKeyTile >> a.page_shift;  // pages per tile
+    my_page = lane & (ppt - 1);
+    my_half = lane / ppt;
+  }
+
+  // Tiles of one piece; a lane copies one page's rows of one half of the channels.
+  template <bool V>
+  __device__ __forceinline__ bool tiles(const ChunkSeg& g) {
+    const int nt = g.i1 - g.i0, shift = a.page_shift;
+    const int s_hi = g.s0 + g.ntok - 1, last_page = (g.L - 1) >> shift;
+    const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
+    // first page that any row's window reaches; pages of the sink below it
+    const int win_page =
+        a.shape.window > 0 ? max(0, g.s0 - a.shape.window + 1) >> shift : 0;
+    const int sink_pages = (a.shape.sink + (1 << shift) - 1) >> shift;
+    int p0 = -1, p1 = -1, p2 = -1;  // physical pages of tiles i, i + 1, i + 2 (-1: none)
+    for (int i = -3; i < nt; ++i) {
+      int p3 = -1;
+      if (i + 3 < nt && my_half < Y::kHalves) {
+        const int lp = tile_of(g, g.i0 + i + 3) * ppt + my_page;
+        if (lp <= last_page && (lp >= win_page || lp < sink_pages)) {
+          p3 = row[lp];
+          if (p3 < 0 || p3 >= a.n_pool) {
+            if ((lp << shift) <= s_hi) report(a.shape.status, SA_ERR_DEVICE_CHECK);
+            p3 = -1;
+          }
+        }
+      }
+      if (i >= 0) {
+        const int x = g.it0 + (V ? v_pos(g.split, nt, i) : k_pos(g.split, i));
+        const int st = x % Y::kStages;
+        if (x >= Y::kStages && !tc::wait_warp(&mi.empty[st], (x / Y::kStages - 1) & 1, &mi.quit,
+                                              a.shape.status))
+          return false;
+        const unsigned m = __ballot_sync(0xffffffffu, p0 >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&mi.full[st], __popc(m) * a.P * 128);
+        __syncwarp();
+        if (p0 >= 0)
+          tc::tma_2d(smem + Y::kRing + st * Y::kTileBytes + my_half * kHalfBytes +
+                         ((uint32_t)my_page << shift) * 128,
+                     map, my_half * 64, (p0 * a.Hkv + g.h) << shift, &mi.full[st]);
+      }
+      p0 = p1;
+      p1 = p2;
+      p2 = p3;
+    }
+    return true;
+  }
+
+  // given up: copies in flight land (bounded) before shared memory goes away
+  __device__ void drain() {
+    for (int st = 0; st < Y::kStages; ++st)
+      for (int ph = 0; ph < 2; ++ph) mbar_wait(&mi.full[st], ph);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void produce_k(const Args& a, uint32_t smem, Misc& mi,
+                                          const CUtensorMap* qmap, const CUtensorMap* kmap) {
+  using Y = Lay<D>;
+  Loader<D> load(a, smem, mi, kmap);
+  const int lane = load.lane;
   ChunkSched sched;
   if (lane == 0) a.cut[blockIdx.x].nparts = 0;
   sched.init(a.shape, blockIdx.x, gridDim.x);
-  const int ppt = kKeyTile >> a.page_shift;  // pages per tile
-  const int my_page = lane % ppt, my_half = lane / ppt;
-  const bool loads = my_half < Y::kHalves;
   int it = 0;
-  bool ok = true;
   for (int n = 0;; ++n) {
     const int slot = n % kSegs;
     if (n >= kSegs && !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit,
-                                     a.shape.status)) {
-      ok = false;
+                                     a.shape.status))
       break;
-    }
     ChunkSeg g;
     const bool more = sched.next(g);
     if (!more) g.valid = 0;
@@ -105,13 +179,10 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
       mbar_arrive(&mi.seg_full[slot]);
       if (more && g.nparts > 0) a.cut[blockIdx.x] = ChunkCut{g.nparts, g.row0, g.ntok, g.h};
     }
-    if (!more) break;
+    if (!more) return;
     // queries: the box is G heads of TB tokens; rows behind the block belong to other
     // sequences (or none) and their results are not kept
-    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, a.shape.status)) {
-      ok = false;
-      break;
-    }
+    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, a.shape.status)) break;
     const int ntile = g.split ? 1 : 2;
     if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, ntile * Y::kHalves * a.TB * a.G * 128);
     __syncwarp();
@@ -120,63 +191,27 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
       tc::tma_3d(smem + Y::kQ + t * Y::kTileBytes + hf * kHalfBytes, qmap, hf * 64, g.h * a.G,
                  g.row0 + t * a.TB, &mi.q_full);
     }
-    // K and V tiles: K of the first tile(s), then V of a tile and K of the next without one
-    const int nt = g.i1 - g.i0, ahead = g.split ? 2 : 1;
-    const int s_hi = g.s0 + g.ntok - 1;
-    const int last_page = (g.L - 1) >> a.page_shift;
-    const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
-    // first page that any row's window reaches; pages of the sink below it
-    const int win_page =
-        a.shape.window > 0 ? max(0, g.s0 - a.shape.window + 1) >> a.page_shift : 0;
-    const int sink_pages = (a.shape.sink + (1 << a.page_shift) - 1) >> a.page_shift;
-    // physical page of this lane's part of tile i of the piece: -1 nothing to load there
-    auto lookup = [&](int i) -> int {
-      if (i >= nt) return -1;
-      const int kt = tile_of(g, g.i0 + i);
-      const int lp = kt * ppt + my_page;
-      if (!loads || lp > last_page || (lp << a.page_shift) > (s_hi | (kKeyTile - 1))) return -1;
-      if (lp < win_page && lp >= sink_pages) return -1;
-      const int ph = row[lp];
-      if (ph < 0 || ph >= a.n_pool) {
-        if ((lp << a.page_shift) <= s_hi) report(a.shape.status, SA_ERR_DEVICE_CHECK);
-        return -1;
-      }
-      return ph;
-    };
-    auto load = [&](const CUtensorMap* map, int ph) -> bool {
-      const int st = it % Y::kStages;
-      if (it >= Y::kStages && !tc::wait_warp(&mi.empty[st], (it / Y::kStages - 1) & 1, &mi.quit,
-                                             a.shape.status))
-        return false;
-      const unsigned m = __ballot_sync(0xffffffffu, ph >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(&mi.full[st], __popc(m) * a.P * 128);
-      __syncwarp();
-      if (ph >= 0)
-        tc::tma_2d(smem + Y::kRing + st * Y::kTileBytes + my_half * kHalfBytes +
-                       ((uint32_t)my_page << a.page_shift) * 128,
-                   map, my_half * 64, (ph * a.Hkv + g.h) << a.page_shift, &mi.full[st]);
-      ++it;
-      return true;
-    };
-    int p0 = lookup(0), p1 = lookup(1), p2 = lookup(2), p3 = lookup(3);
-    ok = load(kmap, p0);
-    if (ok && ahead == 2 && nt > 1) ok = load(kmap, p1);
-    for (int i = 0; ok && i < nt; ++i) {
-      const int p4 = lookup(i + 4);
-      ok = load(vmap, p0);
-      if (ok && i + ahead < nt) ok = load(kmap, ahead == 1 ? p1 : p2);
-      p0 = p1;
-      p1 = p2;
-      p2 = p3;
-      p3 = p4;
-    }
-    if (!ok) break;
+    if (!load.template tiles<false>(g)) break;
+    it += 2 * (g.i1 - g.i0);
   }
-  if (!ok) {  // given up: let copies in flight land (bounded) before shared memory goes away
-    for (int x = max(0, it - Y::kStages); x < it; ++x)
-      mbar_wait(&mi.full[x % Y::kStages], (x / Y::kStages) & 1);
-    mbar_wait(&mi.q_full, 0);
+  load.drain();
+  mbar_wait(&mi.q_full, 0);
+}
+
+template <int D>
+__device__ __forceinline__ void produce_v(const Args& a, uint32_t smem, Misc& mi,
+                                          const CUtensorMap* vmap) {
+  Loader<D> load(a, smem, mi, vmap);
+  for (int n = 0;; ++n) {
+    const int slot = n % kSegs;
+    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, a.shape.status)) break;
+    const ChunkSeg g = mi.seg[slot];
+    __syncwarp();
+    if (load.lane == 0) mbar_arrive(&mi.seg_empty[slot]);
+    if (!g.valid) return;
+    if (!load.template tiles<true>(g)) break;
   }
+  load.drain();
 }
 
 // ---- one warp issues every product ----------------------------------------------------
@@ -204,17 +239,25 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
     }
     tc::commit(&mi.s_full[t]);
   };
-  auto values = [&](int t, int x, bool first) {  // O_t += P_t V of stage x
+  // O_t += P_t V of stage x, as the halves of P_t come; `then` follows in the same lane
+  auto values = [&](int t, int x, bool first, auto then) -> bool {
     const uint32_t v = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
+    const uint32_t parity = np[t]++ & 1;
 #pragma unroll
-    for (int kk = 0; kk < kKeyTile / 16; ++kk)
-      tc::mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8,
-                 tc::desc(v + kk * 2048, kHalfBytes), id_o, !(first && kk == 0));
-  };
-  auto probs = [&](int t) {  // P_t is there
-    const bool r = tc::wait_warp(&mi.p_full[t], np[t]++ & 1, &mi.quit, status);
-    tc::fence_after();
-    return r;
+    for (int hf = 0; hf < 2; ++hf) {
+      if (!tc::wait_warp(hf ? &mi.p_full[t] : &mi.p_half[t], parity, &mi.quit, status))
+        return false;
+      tc::fence_after();
+      if (tc::elect()) {
+#pragma unroll
+        for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
+          tc::mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8,
+                     tc::desc(v + kk * 2048, kHalfBytes), id_o, !(first && kk == 0));
+        if (hf) then();
+      }
+      __syncwarp();
+    }
+    return true;
   };
   for (int n = 0;; ++n) {
     const int slot = n % kSegs;
@@ -239,30 +282,25 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
         const int v = it++;
         const bool more = i + 1 < nt;
         if (more) k = it++;
-        if (!staged(v) || !probs(0)) return;
-        if (tc::elect()) {
-          values(0, v, i == 0);
-          if (!more) tc::commit(&mi.o_full[0]);
-        }
-        __syncwarp();
-        if (more) {
-          if (!staged(k)) return;
-          if (tc::elect()) scores(0, 0, k);
-          __syncwarp();
-        }
-        if (!probs(1)) return;
-        if (tc::elect()) {
-          values(1, v, i == 0);
-          tc::commit(&mi.empty[v % Y::kStages]);
-          if (more) {
-            scores(1, 1, k);
-            tc::commit(&mi.empty[k % Y::kStages]);
-            if (i + 2 == nt) tc::commit(&mi.q_empty);
-          } else {
-            tc::commit(&mi.o_full[1]);
-          }
-        }
-        __syncwarp();
+        if (!staged(v) || (more && !staged(k))) return;
+        if (!values(0, v, i == 0, [&] {
+              if (more)
+                scores(0, 0, k);
+              else
+                tc::commit(&mi.o_full[0]);
+            }))
+          return;
+        if (!values(1, v, i == 0, [&] {
+              tc::commit(&mi.empty[v % Y::kStages]);
+              if (more) {
+                scores(1, 1, k);
+                tc::commit(&mi.empty[k % Y::kStages]);
+                if (i + 2 == nt) tc::commit(&mi.q_empty);
+              } else {
+                tc::commit(&mi.o_full[1]);
+              }
+            }))
+          return;
       }
     } else {
       for (int i = 0; i < min(nt, 2); ++i) {
@@ -277,13 +315,12 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
       }
       for (int i = 0; i < nt; ++i) {
         const int t = i & 1, v = it++;
-        if (!staged(v) || !probs(t)) return;
-        if (tc::elect()) {
-          values(t, v, i < 2);
-          tc::commit(&mi.empty[v % Y::kStages]);
-          if (i + 2 >= nt) tc::commit(&mi.o_full[t]);
-        }
-        __syncwarp();
+        if (!staged(v)) return;
+        if (!values(t, v, i < 2, [&] {
+              tc::commit(&mi.empty[v % Y::kStages]);
+              if (i + 2 >= nt) tc::commit(&mi.o_full[t]);
+            }))
+          return;
         if (i + 2 < nt) {
           const int k = it++;
           if (!staged(k)) return;
@@ -299,9 +336,14 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
   }
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  return fmaxf(fmaxf(a, b), c);
+// bit c: c < n
+__device__ __forceinline__ uint32_t below(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1;
 }
+
+// Of every kPolyOf pairs of probabilities the last kPoly are computed on the FMA pipes: the 16
+// exponentials a cycle of an SM's special-function unit would take as long as both products.
+constexpr int kPolyOf = 4, kPoly = 0;
 
 // ---- softmax and epilogue of chain t (four warps, thread = row) --------------------------
 template <int D>
@@ -343,7 +385,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
       const bool ragged = key0 + kKeyTile > g.L || lo_row > 0 ||
                           (a.shape.window > 0 && key0 < a.shape.sink);
       if (ragged && (g.split || t == 0)) {
-        const int x = g.it0 + (g.split ? (ti + 1 < nt ? 2 + 2 * ti : 2 * nt - 1) : 1 + 2 * ti);
+        const int x = g.it0 + v_pos(g.split, nt, ti);
         if (!tc::wait_warp(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status))
           return;
         const int key = key0 + r, page = key >> a.page_shift;
@@ -368,15 +410,25 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         const int hi = s - key0, lo = a.shape.window > 0 ? hi - a.shape.window : -1;
         const int sk = a.shape.sink - key0;
         // some key of the tile hidden from some row of the warp
-        if (__any_sync(0xffffffffu, real && (hi < kKeyTile - 1 || (lo >= 0 && sk <= min(lo, kKeyTile - 1))))) {
+        if (__any_sync(0xffffffffu, real && (hi < kKeyTile - 1 ||
+                                             (lo >= 0 && sk <= min(lo, kKeyTile - 1))))) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(c <= hi && (c > lo || c < sk))) x[c] = 0xFF800000u;  // -inf
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            const uint32_t see =
+                below(hi + 1 - c0) & (~below(lo + 1 - c0) | below(sk - c0));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((see >> c) & 1)) x[c0 + c] = 0xFF800000u;  // -inf
+          }
         }
-        float mx = -INFINITY;
+        float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          mx = max3(mx, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        for (int c = 0; c < 128; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mxs[e] = tc::max3(mxs[e], __uint_as_float(x[c + 2 * e]),
+                              __uint_as_float(x[c + 2 * e + 1]));
+        float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
         mx *= a.scale_log2;
         if (i == 0) {
           m = mx;
@@ -396,24 +448,50 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sl2 = tc::pair(a.scale_log2, a.scale_log2), off2 = tc::pair(off, off);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 64) {
           uint32_t p[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float p0 =
-                fast_exp2(fmaf(__uint_as_float(x[c0 + c]), a.scale_log2, off));
-            const float p1 =
-                fast_exp2(fmaf(__uint_as_float(x[c0 + c + 1]), a.scale_log2, off));
-            sum[(c >> 1) & 1] += p0;
-            sum[((c >> 1) & 1) + 2] += p1;
-            p[c >> 1] = pack_bf16(p0, p1);
+          for (int b0 = 0; b0 < 64; b0 += 32) {
+            uint64_t y[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              y[c] = tc::fma2(tc::pair(__uint_as_float(x[c0 + b0 + 2 * c]),
+                                       __uint_as_float(x[c0 + b0 + 2 * c + 1])),
+                              sl2, off2);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float p0, p1;
+              if (c % kPolyOf >= kPolyOf - kPoly) {
+                tc::exp2_poly(y[c], p0, p1);
+              } else {
+                tc::unpair(y[c], p0, p1);
+                p0 = fast_exp2(p0);
+                p1 = fast_exp2(p1);
+              }
+              y[c] = tc::pair(p0, p1);
+              p[(b0 >> 1) + c] = pack_bf16(p0, p1);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum[c & 1] = tc::add2(sum[c & 1], y[c]);
           }
           tc::tmem_st32(s_col + (c0 >> 1), p);
+          if (c0 == 0) {  // the product over the first 64 keys may start
+            tc::tmem_wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mi.p_half[t]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float a0, a1, a2, a3;
+        tc::unpair(sum[0], a0, a1);
+        tc::unpair(sum[1], a2, a3);
+        l += (a0 + a1) + (a2 + a3);
         tc::tmem_wait_st();
+      } else if (lane == 0) {
+        mbar_arrive(&mi.p_half[t]);
       }
       tc::fence_before();
       __syncwarp();
@@ -523,7 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_u32(smem_raw);
   Misc& mi = *reinterpret_cast<Misc*>(smem_raw + Y::kMisc);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 352) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
   if (tid == 0) {
     for (int i = 0; i < Y::kStages; ++i) {
       mbar_init(&mi.full[i], 1);
@@ -531,12 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&mi.seg_full[i], 1);
-      mbar_init(&mi.seg_empty[i], 9);  // the issuing thread and eight softmax warps
+      mbar_init(&mi.seg_empty[i], 10);  // V's, the products' and the eight softmax warps
     }
     mbar_init(&mi.q_full, 1);
     mbar_init(&mi.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&mi.s_full[t], 1);
+      mbar_init(&mi.p_half[t], 4);
       mbar_init(&mi.p_full[t], 4);
       mbar_init(&mi.o_full[t], 1);
     }
@@ -553,17 +637,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = mi.tmem;
   if (warp < 8) {
+    tc::regs_up<kSoftmaxRegs>();
     soften<D>(a, smem, mi, tmem, warp >> 2);
-  } else if (warp == 8) {
-    multiply<D>(a, smem, mi, tmem);
-    __syncwarp();
-    if (tc::elect()) {
-      tc::commit(&mi.drain);
-      mbar_wait(&mi.drain, 0);
-    }
-    __syncwarp();
   } else {
-    produce<D>(a, smem, mi, &qmap, &kmap, &vmap);
+    tc::regs_down<kOtherRegs>();
+    if (warp == 8) {
+      multiply<D>(a, smem, mi, tmem);
+      __syncwarp();
+      if (tc::elect()) {
+        tc::commit(&mi.drain);
+        mbar_wait(&mi.drain, 0);
+      }
+    } else if (warp == 9) {
+      produce_k<D>(a, smem, mi, &qmap, &kmap);
+    } else if (warp == 10) {
+      produce_v<D>(a, smem, mi, &vmap);
+    }
     __syncwarp();
   }
   tc::fence_before();

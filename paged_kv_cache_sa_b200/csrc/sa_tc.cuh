@@ -113,6 +113,63 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* q
   return __all_sync(0xffffffffu, wait(bar, parity, quit, status));
 }
 
+// ---- arithmetic on pairs of fp32 (one instruction for both) ------------------------------
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^a and 2^b on the FMA pipes, for arguments below 128: y = n + f with n the nearest integer
+// (adding 1.5 * 2^23 leaves it in the low bits), 2^f by a cubic on [-1/2, 1/2] fitted to the
+// least relative error (7.5e-5, a twentieth of half a bf16 step), n added to the exponent.
+// Below 2^-126 the result is 0 (an exact one for masked scores).
+__device__ __forceinline__ void exp2_poly(uint64_t y, float& a, float& b) {
+  float ya, yb;
+  unpair(y, ya, yb);
+  y = pair(fmaxf(ya, -150.f), fmaxf(yb, -150.f));
+  const uint64_t magic = pair(12582912.f, 12582912.f);
+  const uint64_t t = add2(y, magic);
+  const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), y);
+  uint64_t p = fma2(f, pair(5.5171624e-2f, 5.5171624e-2f), pair(2.4261113e-1f, 2.4261113e-1f));
+  p = fma2(p, f, pair(6.9326097e-1f, 6.9326097e-1f));
+  p = fma2(p, f, pair(9.9992806e-1f, 9.9992806e-1f));
+  float ta, tb;
+  unpair(t, ta, tb);
+  unpair(p, a, b);
+  a = __int_as_float(max((int)((__float_as_uint(ta) << 23) + __float_as_uint(a)), 0));
+  b = __int_as_float(max((int)((__float_as_uint(tb) << 23) + __float_as_uint(b)), 0));
+}
+
+// Registers per thread of a warpgroup (four warps, all of them call it): the shares of a block
+// add up to no more than it was launched with.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // tiled TMA loads global -> shared (no multicast); x * 2 bytes is a multiple of 16
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                        uint64_t* bar) {
