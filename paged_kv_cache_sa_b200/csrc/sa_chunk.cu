@@ -65,7 +65,7 @@ struct Args {
   const int32_t* page_table;
   uint16_t* out;
   float* lse;
-  float* part_o;    // [2 n_cta][rows_cap][D]
+  float* part_o;    // [2 n_cta][rows_cap / 8][D / 4][8][4]
   float2* part_ml;  // [2 n_cta][rows_cap]
   ChunkCut* cut;    // [n_cta]
   int rows_cap;
@@ -114,6 +114,8 @@ struct Loader {
     const int win_page =
         a.shape.window > 0 ? max(0, g.s0 - a.shape.window + 1) >> shift : 0;
     const int sink_pages = (a.shape.sink + (1 << shift) - 1) >> shift;
+    // keys that no other CTA reads leave L2 first: what every call starts from stays in it
+    const uint64_t policy = g.once ? l2_evict_first() : tc::l2_normal();
     int p0 = -1, p1 = -1, p2 = -1;  // physical pages of tiles i, i + 1, i + 2 (-1: none)
     for (int i = -3; i < nt; ++i) {
       int p3 = -1;
@@ -139,7 +141,7 @@ struct Loader {
         if (p0 >= 0)
           tc::tma_2d(smem + Y::kRing + st * Y::kTileBytes + my_half * kHalfBytes +
                          ((uint32_t)my_page << shift) * 128,
-                     map, my_half * 64, (p0 * a.Hkv + g.h) << shift, &mi.full[st]);
+                     map, my_half * 64, (p0 * a.Hkv + g.h) << shift, &mi.full[st], policy);
       }
       p0 = p1;
       p1 = p2;
@@ -498,39 +500,14 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
       if (lane == 0) mbar_arrive(&mi.p_full[t]);
     }
     // ---- results: whole items are normalised and rounded, pieces leave (O, m, l)
-    const size_t orow = ((size_t)(g.row0 + tk) * a.Hq + g.h * a.G + gh);
+    const int64_t orow = (int64_t)(g.row0 + tk) * a.Hq + g.h * a.G + gh;
     const size_t prow = (size_t)max(g.part, 0) * a.rows_cap + (g.split ? 0 : t * 128) + r;
+    int c_from = 0, c_to = D;
+    float f0 = 1.f, f1 = 0.f;  // weights of the two accumulators
+    uint32_t o_col = tmem + lanes + 256 + t * D;
     if (!g.split) {
       if (!tc::wait_warp(&mi.o_full[t], no[t]++ & 1, &mi.quit, status)) return;
       ++no[1 - t];  // the other chain's completes too; its warps wait for it
-      tc::fence_after();
-      if (any) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32(tmem + lanes + 256 + t * D + c0, o);
-          if (real && g.part >= 0) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                   __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-          } else if (real) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(o[8 * c + 2 * e]) * inv,
-                                 __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
-              dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          __syncwarp();
-        }
-      }
     } else {
       // both chains hold a state of the same rows: exchange (m, l), then each group of warps
       // writes half of the channels
@@ -540,54 +517,87 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
       if (!tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status)) return;
       if (!tc::wait_warp(&mi.o_full[0], no[0]++ & 1, &mi.quit, status)) return;
       if (nt > 1 && !tc::wait_warp(&mi.o_full[1], no[1]++ & 1, &mi.quit, status)) return;
-      tc::fence_after();
-      if (any) {
-        const float2 s0 = mi.ml[0][r], s1 = mi.ml[1][r];
-        m = fmaxf(s0.x, s1.x);
-        const float f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
-        const float f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
-        l = s0.y * f0 + s1.y * f1;
-        const float inv = g.part >= 0 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const float2 s0 = mi.ml[0][r], s1 = mi.ml[1][r];
+      m = fmaxf(s0.x, s1.x);
+      f0 = s0.x == -INFINITY ? 0.f : fast_exp2(s0.x - m);
+      f1 = s1.x == -INFINITY ? 0.f : fast_exp2(s1.x - m);
+      l = s0.y * f0 + s1.y * f1;
+      o_col = tmem + lanes + 256;
+      c_from = t * (D / 2);
+      c_to = c_from + D / 2;
+    }
+    tc::fence_after();
+    if (any) {
+      if (g.part < 0) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+      }
 #pragma unroll 1
-        for (int c0 = t * (D / 2); c0 < (t + 1) * (D / 2); c0 += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32(tmem + lanes + 256 + c0, o);
-          float v[32];
+      for (int c0 = c_from; c0 < c_to; c0 += 32) {
+        uint32_t o[32];
+        tc::tmem_ld32(o_col + c0, o);
+        float v[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(o[c]) * f0;
-          if (nt > 1) {
-            tc::tmem_ld32(tmem + lanes + 256 + D + c0, o);
+        for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(o[c]) * f0;
+        if (g.split && nt > 1) {
+          tc::tmem_ld32(o_col + D + c0, o);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(o[c]) * f1;
-          }
-          if (real && g.part >= 0) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c0);
+          for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(o[c]) * f1;
+        }
+        if (g.part >= 0) {
+          // [8 rows][D / 4][8][4]: a warp's store is four runs of 128 bytes
+          float4* dst = reinterpret_cast<float4*>(a.part_o) +
+                        ((prow >> 3) * (D / 4) + (c0 >> 2)) * 8 + (r & 7);
+          if (real) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          } else if (real) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              dst[c] = make_uint4(pack_bf16(v[8 * c] * inv, v[8 * c + 1] * inv),
-                                  pack_bf16(v[8 * c + 2] * inv, v[8 * c + 3] * inv),
-                                  pack_bf16(v[8 * c + 4] * inv, v[8 * c + 5] * inv),
-                                  pack_bf16(v[8 * c + 6] * inv, v[8 * c + 7] * inv));
+              dst[c * 8] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
           }
-          __syncwarp();
+        } else {
+          // four lanes turn their rows' 64 bytes, so that a store covers 64 bytes of a row
+          uint32_t w[4][4];  // [16-byte unit][word]
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c >> 2][c & 3] = pack_bf16(v[2 * c], v[2 * c + 1]);
+#pragma unroll
+          for (int o2 = 1; o2 < 4; o2 <<= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (!(u & o2)) {
+                const bool odd = lane & o2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t got = __shfl_xor_sync(
+                      0xffffffffu, odd ? w[u][e] : w[u | o2][e], o2);
+                  if (odd)
+                    w[u][e] = got;
+                  else
+                    w[u | o2][e] = got;
+                }
+              }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // row k of the four
+            const int64_t to = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
+            if (__shfl_sync(0xffffffffu, real, (lane & ~3) + k))
+              *reinterpret_cast<uint4*>(a.out + to * D + c0 + (lane & 3) * 8) =
+                  make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+          }
         }
+        __syncwarp();
       }
+      if (real && (!g.split || t == 0)) {
+        if (g.part >= 0)
+          a.part_ml[prow] = make_float2(m, l);
+        else
+          a.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+    }
+    tc::fence_before();
+    if (g.split) {
       // the other chain's accumulator and state may be overwritten once all have read them
-      tc::fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&mi.meet);
       if (!tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status)) return;
-    }
-    if (real && (!g.split || t == 0)) {
-      if (g.part >= 0)
-        a.part_ml[prow] = make_float2(m, l);
-      else
-        a.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
   }
 }
@@ -661,84 +671,97 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
-// Joins the pieces of the cut items: out = sum_p 2^(m_p - M) O_p / L, in piece order.  A row
-// is one warp's (SPLIT: a CTA's, whose eight warps take every eighth piece), a lane holds
-// D / 32 channels.  Also returns the item counter to zero for the next call.
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ part_o,
+// Joins the pieces of the cut items: out = sum_p 2^(m_p - M) O_p / L.  A CTA has eight rows of
+// one item; its eight warps take every eighth piece, a lane one row and every fourth 16-byte
+// group of its channels; the warps' sums meet in shared memory in warp order.  Also returns the
+// item counter to zero for the next call.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ part_o,
                                                    const float2* __restrict__ part_ml,
                                                    const ChunkCut* __restrict__ cut,
                                                    int32_t* ticket, uint16_t* __restrict__ out,
                                                    float* __restrict__ lse, int rows_cap, int Hq,
                                                    int G, int TB) {
-  constexpr int C = D / 32;
-  __shared__ float acc_s[8][D];
-  __shared__ float2 ml_s[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int C = D / 16;  // 16-byte groups of a lane
+  __shared__ float4 acc_s[8][D / 4][8];
+  __shared__ float2 ml_s[8][8];
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   if (c == 0 && blockIdx.y == 0 && threadIdx.x == 0) *ticket = 0;
   const ChunkCut k = cut[c];
-  const int r = SPLIT ? blockIdx.y : blockIdx.y * 8 + warp;
-  const int tile = r >> 7, tok = (r & 127) / G, gh = (r & 127) % G, tk = tok + tile * TB;
-  if (k.nparts <= 0 || tok >= TB || tk >= k.ntok) return;  // per warp, or per CTA (SPLIT)
-  float M = -INFINITY, l = 0.f, acc[C];
+  if (k.nparts <= 0) return;
+  const int r0 = blockIdx.y * 8;
+  {  // nothing to do behind the item's last row
+    const int tok = (r0 & 127) / G + (r0 >> 7) * TB;
+    if (tok >= k.ntok) return;
+  }
+  const int r8 = lane & 7, sub = lane >> 3;
+  auto slot = [&](int p) {
+    return ((size_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_cap + r0);
+  };
+  float M = -INFINITY, l = 0.f;
+  float4 acc[C];
 #pragma unroll
-  for (int e = 0; e < C; ++e) acc[e] = 0.f;
-  auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_cap + r; };
-  const int p0 = SPLIT ? warp : 0, step = SPLIT ? 8 : 1;
-  for (int p = p0 + lane * step; p < k.nparts; p += 32 * step) M = fmaxf(M, part_ml[slot(p)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 4
-  for (int p = p0; p < k.nparts; p += step) {
-    const float2 ml = part_ml[slot(p)];
-    const float* src = part_o + slot(p) * D + lane * C;
-    float v[C];
-#pragma unroll
-    for (int e = 0; e < C; e += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + e);
-      v[e] = x.x;
-      v[e + 1] = x.y;
-    }
+  for (int e = 0; e < C; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = warp + 8 * sub; p < k.nparts; p += 32) M = fmaxf(M, part_ml[slot(p) + r8].x);
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+#pragma unroll 2
+  for (int p = warp; p < k.nparts; p += 8) {
+    const size_t at = slot(p);
+    const float2 ml = part_ml[at + r8];
+    const float4* src = part_o + ((at >> 3) * (D / 4) + sub) * 8 + r8;
     const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
     l += f * ml.y;
 #pragma unroll
-    for (int e = 0; e < C; ++e) acc[e] += f * v[e];
-  }
-  if (SPLIT) {
-#pragma unroll
-    for (int e = 0; e < C; ++e) acc_s[warp][lane * C + e] = acc[e];
-    if (lane == 0) ml_s[warp] = make_float2(M, l);
-    __syncthreads();
-    if (warp) return;
-    float W = -INFINITY;
-    for (int w = 0; w < 8; ++w) W = fmaxf(W, ml_s[w].x);
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < C; ++e) acc[e] = 0.f;
-    for (int w = 0; w < 8; ++w) {
-      const float2 ml = ml_s[w];
-      const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - W);
-      l += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < C; ++e) acc[e] += f * acc_s[w][lane * C + e];
+    for (int e = 0; e < C; ++e) {
+      const float4 v = src[e * 32];
+      acc[e].x += f * v.x;
+      acc[e].y += f * v.y;
+      acc[e].z += f * v.z;
+      acc[e].w += f * v.w;
     }
-    M = W;
+  }
+#pragma unroll
+  for (int e = 0; e < C; ++e) acc_s[warp][4 * e + sub][r8] = acc[e];
+  if (sub == 0) ml_s[warp][r8] = make_float2(M, l);
+  __syncthreads();
+  const int row = warp, r = r0 + row;  // a warp writes one row
+  const int tok = (r & 127) / G, gh = (r & 127) % G, tk = tok + (r >> 7) * TB;
+  if (tok >= TB || tk >= k.ntok) return;
+  float W = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) W = fmaxf(W, ml_s[w][row].x);
+  l = 0.f;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float2 ml = ml_s[w][row];
+    if (ml.x == -INFINITY) continue;
+    const float f = fast_exp2(ml.x - W);
+    l += f * ml.y;
+    if (lane < D / 4) {
+      const float4 v = acc_s[w][lane][row];
+      sum.x += f * v.x;
+      sum.y += f * v.y;
+      sum.z += f * v.z;
+      sum.w += f * v.w;
+    }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t orow = (size_t)(k.row0 + tk) * Hq + k.h * G + gh;
-#pragma unroll
-  for (int e = 0; e < C; e += 2)
-    *reinterpret_cast<uint32_t*>(out + orow * D + lane * C + e) =
-        pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  const int64_t orow = (int64_t)(k.row0 + tk) * Hq + k.h * G + gh;
+  if (lane < D / 4)
+    reinterpret_cast<uint2*>(out + orow * D)[lane] =
+        make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
   if (lane == 0)
-    lse[orow] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    lse[orow] = l > 0.f ? (W + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 static int rows_cap(const sa_geom& g, int n_tokens) {
   const int G = g.Hq / g.Hkv, TB = 128 / G;
-  return n_tokens > TB ? 256 : (n_tokens > 0 ? n_tokens : 1) * G;
+  return n_tokens > TB ? 256 : ((n_tokens > 0 ? n_tokens : 1) * G + 7) & ~7;
 }
 
 template <int D>
@@ -791,13 +814,10 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   if (e != cudaSuccess) return e;
   void* args[] = {&qm, &km, &vm, &a};
   if ((e = chunk_launch(fn, dim3(c.n_sm), kThreads, Y::kSmem, stream, args)) != cudaSuccess) return e;
-  const bool split = a.rows_cap <= 64;
-  const dim3 grid(c.n_sm, split ? a.rows_cap : (a.rows_cap + 7) / 8);
-  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut,      &a.shape.ticket, &a.out,
+  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.shape.ticket, &a.out,
                    &a.lse,    &a.rows_cap, &a.Hq, &a.G, &a.TB};
-  return chunk_launch(split ? reinterpret_cast<const void*>(join_kernel<D, true>)
-                      : reinterpret_cast<const void*>(join_kernel<D, false>),
-                grid, 256, 0, stream, jargs);
+  return chunk_launch(reinterpret_cast<const void*>(join_kernel<D>),
+                      dim3(c.n_sm, a.rows_cap / 8), 256, 0, stream, jargs);
 }
 
 static size_t bytes(const sa_geom& g, int n_tokens, int n_sm) {

@@ -37,7 +37,7 @@ struct ChunkSeg {
   int part;        // workspace slot of a cut piece, -1 for a whole item
   int nparts;      // of a cut item, at its first piece (0 elsewhere)
   int it0;         // stages the producer has filled before this piece
-  int pad;
+  int once;        // no other block reads these keys
 };
 static_assert(sizeof(ChunkSeg) == 64, "segment is 64 bytes");
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkShape& s, int n, in
   if (s.window > 0) {
     const int first = max(0, lo - s.window + 1);  // lowest key of any row's window
     k.bs = first / kKeyTile;
-    k.na = min((int)(((int64_t)min(s.sink, hi + 1) + kKeyTile - 1) / kKeyTile), k.bs);
+    k.na = min((min(s.sink, hi + 1) + kKeyTile - 1) / kKeyTile, k.bs);
   }
   k.tiles = k.na + hi / kKeyTile - k.bs + 1;
   k.split = k.nt <= s.ST;
@@ -92,54 +92,36 @@ __device__ __forceinline__ bool chunk_seq(const ChunkShape& s, int b, int& c0, i
   return ok;
 }
 
-// Every member function is called by one whole warp.
+__device__ __forceinline__ uint32_t warp_prefix(uint32_t v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// The list is made by every CTA for itself, before its first copy, by code that runs once: it
+// is kept short and free of divisions.  Every member function is called by one whole warp.
 struct ChunkSched {
   ChunkShape s;
-  int nc, c;             // runs, and this CTA's
+  int runs, c;           // runs that the CTAs could take, and this CTA's
   int lane_h;            // its head group (inner > 1)
   bool whole;
-  int64_t total, left;   // steps of all items; of this CTA still to hand out
-  int64_t pos;           // steps before the current item
+  uint32_t total, left;  // steps of all items (cut list); of this run still to hand out
+  uint32_t per, rem;     // total = per * runs + rem
+  uint32_t pos;          // steps before the current item
   int b, h, j, off;      // the current item and how many of its steps are gone
   int n, L, c0;          // its sequence
   int items, ticket;     // whole items: count, and the next one drawn
   int gb, gpre;          // whole items: group of 32 sequences, items before it
 
-  // steps of all blocks (one head) of sequence (nn, LL) of this lane, and the longest
-  __device__ __forceinline__ int64_t seq_steps(int nn, int LL, int& longest) {
-    const int lane = threadIdx.x & 31;
-    const int nb = (nn + s.BT - 1) / s.BT;
-    int64_t sum = 0;
-    int most = 0;
-    if (nb <= 4)
-      for (int q = 0; q < nb; ++q) {
-        const int st = chunk_block(s, nn, LL, q).steps;
-        sum += st;
-        most = max(most, st);
-      }
-    for (unsigned m = __ballot_sync(0xffffffffu, nb > 4); m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int n1 = __shfl_sync(0xffffffffu, nn, src), L1 = __shfl_sync(0xffffffffu, LL, src);
-      const int nb1 = (n1 + s.BT - 1) / s.BT;
-      int64_t t = 0;
-      int mx = 0;
-      for (int q = lane; q < nb1; q += 32) {
-        const int st = chunk_block(s, n1, L1, q).steps;
-        t += st;
-        mx = max(mx, st);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      if (lane == src) {
-        sum = t;
-        most = mx;
-      }
-    }
-    longest = most;
-    return sum;
+  __device__ __forceinline__ int blocks(int nn) const {
+    return nn <= s.BT ? nn > 0 : (nn + s.BT - 1) / s.BT;
   }
 
+  // sequence of this lane in the group from `base`: its new tokens and length
   __device__ __forceinline__ void lane_seq(int base, int& nn, int& LL, bool check) {
     const int q = base + (threadIdx.x & 31);
     int cc;
@@ -148,32 +130,69 @@ struct ChunkSched {
     if (q < s.B && !chunk_seq(s, q, cc, nn, LL) && check) report(s.status, SA_ERR_DEVICE_CHECK);
   }
 
-  __device__ void init(const ChunkShape& shape, int cta, int n_cta) {
-    s = shape;
-    c = cta / s.inner;
-    lane_h = cta % s.inner;
-    const int runs = n_cta / s.inner;
+  // steps of all blocks (one head) of this lane's sequence, and of its longest block
+  __device__ __forceinline__ uint32_t seq_steps(int nn, int LL, uint32_t& longest) {
     const int lane = threadIdx.x & 31;
-    total = 0;
+    const int nb = blocks(nn);
+    uint32_t sum = 0, most = 0;
+    // one block at a time by the lane itself, or (many blocks) 32 at a time by the warp
+    for (unsigned todo = __ballot_sync(0xffffffffu, nb > 0); todo;) {
+      const unsigned many = __ballot_sync(0xffffffffu, nb > 1) & todo;
+      const int src = many ? __ffs(many) - 1 : lane;
+      todo = many ? todo & ~(1u << src) : 0;
+      const int n1 = __shfl_sync(0xffffffffu, nn, src), L1 = __shfl_sync(0xffffffffu, LL, src);
+      const int nb1 = blocks(n1);
+      uint64_t t = 0;
+      uint32_t mx = 0;
+#pragma unroll 1
+      for (int q = many ? lane : 0; q < nb1; q += 32) {
+        const uint32_t st = chunk_block(s, n1, L1, q).steps;
+        t += st;
+        mx = max(mx, st);
+      }
+      if (many) {  // saturated at 2^31, where no list is cut
+        const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)min(t >> 24, (uint64_t)255));
+        t = __reduce_add_sync(0xffffffffu, (uint32_t)t & 0xFFFFFFu) + ((uint64_t)hi << 24);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+      }
+      if (many ? lane == src : nb == 1) {
+        sum = (uint32_t)min(t, (uint64_t)1 << 31);
+        most = mx;
+      }
+    }
+    longest = most;
+    return sum;
+  }
+
+  // step that run r starts at, floor(r total / runs), for r <= runs
+  __device__ __forceinline__ uint32_t start(uint32_t r) const { return r * per + r * rem / runs; }
+
+  __device__ __forceinline__ void init(const ChunkShape& shape, int cta, int n_cta) {
+    s = shape;
+    c = s.inner == 1 ? cta : cta / s.inner;
+    lane_h = s.inner == 1 ? 0 : cta % s.inner;
+    runs = s.inner == 1 ? n_cta : n_cta / s.inner;
+    const int lane = threadIdx.x & 31;
+    uint64_t all = 0;
+    uint32_t longest = 0, mine = 0;
     items = 0;
-    int longest = 0;
+#pragma unroll 1
     for (int base = 0; base < s.B; base += 32) {
-      int nn, LL, mx;
+      int nn, LL;
+      uint32_t mx;
       lane_seq(base, nn, LL, cta == 0);
-      int64_t t = seq_steps(nn, LL, mx);
-      int k = (nn + s.BT - 1) / s.BT;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      total += t;
-      items += __reduce_add_sync(0xffffffffu, k);
+      mine = seq_steps(nn, LL, mx);
+      all += __reduce_add_sync(0xffffffffu, mine & 0xFFFFu) +
+             ((uint64_t)__reduce_add_sync(0xffffffffu, mine >> 16) << 16);
+      items += __reduce_add_sync(0xffffffffu, blocks(nn));
       longest = max(longest, __reduce_max_sync(0xffffffffu, mx));
     }
-    total *= s.H;
+    all *= s.H;
     items *= s.H;
-    nc = (int)min((int64_t)runs, total);
-    whole = total >= (int64_t)kWholeFactor * longest * runs;
+    // whole items, too, where a count of steps would not fit 32 bits
+    whole = all >= (uint64_t)kWholeFactor * longest * runs || all >> 31;
     left = 0;
-    if (total == 0) {
+    if (all == 0 || c >= runs) {
       whole = false;
       return;
     }
@@ -183,52 +202,53 @@ struct ChunkSched {
       draw();
       return;
     }
-    if (c >= nc) return;
-    const int64_t x0 = total * c / nc;
-    left = total * (c + 1) / nc - x0;
-    // the item that step x0 belongs to
-    int64_t pre = 0;
-    for (int base = 0; base < s.B; base += 32) {
-      int nn, LL, mx;
-      lane_seq(base, nn, LL, false);
-      const int64_t mine = seq_steps(nn, LL, mx) * s.H;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+    total = (uint32_t)all;
+    if (total < (uint32_t)runs) runs = (int)total;  // a step each
+    per = total / (uint32_t)runs;
+    rem = total - per * runs;
+    if (c >= runs) return;
+    const uint32_t x0 = start(c);
+    left = start(c + 1) - x0;
+    // the sequence and head that step x0 belongs to
+    pos = 0;
+#pragma unroll 1
+    for (int base = 0;; base += 32) {
+      if (s.B > 32) {
+        int nn, LL;
+        uint32_t mx;
+        lane_seq(base, nn, LL, false);
+        mine = seq_steps(nn, LL, mx);
       }
-      const unsigned m = __ballot_sync(0xffffffffu, pre + incl > x0);
-      if (m) {
-        const int src = __ffs(m) - 1;
-        b = base + src;
-        const int64_t cost = __shfl_sync(0xffffffffu, mine, src) / s.H;
-        pos = pre + __shfl_sync(0xffffffffu, incl - mine, src);
-        h = (int)((x0 - pos) / cost);
-        pos += h * cost;
-        break;
-      }
-      pre += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    chunk_seq(s, b, c0, n, L);
-    const int nb = (n + s.BT - 1) / s.BT;
-    for (j = 0; j < nb; j += 32) {
-      const int q = j + lane;
-      const int mine = q < nb ? chunk_block(s, n, L, q).steps : 0;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
+      const uint32_t incl = warp_prefix(mine * s.H);
       const unsigned m = __ballot_sync(0xffffffffu, pos + incl > x0);
       if (m) {
         const int src = __ffs(m) - 1;
-        pos += __shfl_sync(0xffffffffu, incl - mine, src);
-        j += src;
+        b = base + src;
+        const uint32_t cost = __shfl_sync(0xffffffffu, mine, src);
+        pos += __shfl_sync(0xffffffffu, incl, src) - cost * s.H;
+        for (h = 0; x0 - pos >= cost; ++h) pos += cost;
         break;
       }
       pos += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    // and its block
+    chunk_seq(s, b, c0, n, L);
+    j = 0;
+    const int nb = blocks(n);
+    if (nb > 1) {
+#pragma unroll 1
+      for (;; j += 32) {
+        const uint32_t st = j + lane < nb ? chunk_block(s, n, L, j + lane).steps : 0;
+        const uint32_t incl = warp_prefix(st);
+        const unsigned m = __ballot_sync(0xffffffffu, pos + incl > x0);
+        if (m) {
+          const int src = __ffs(m) - 1;
+          pos += __shfl_sync(0xffffffffu, incl - st, src);
+          j += src;
+          break;
+        }
+        pos += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
     off = (int)(x0 - pos);
   }
@@ -237,76 +257,54 @@ struct ChunkSched {
     if ((threadIdx.x & 31) == 0) ticket = atomicAdd(s.ticket, 1);
   }
 
-  // The next piece; false when there is none.
-  __device__ bool next(ChunkSeg& g) {
-    const int lane = threadIdx.x & 31;
-    g.nparts = 0;
-    g.part = -1;
-    if (whole) {
-      const int drawn = __shfl_sync(0xffffffffu, ticket, 0), t = drawn / s.inner;
-      if (t >= items || drawn < 0) return false;
-      lane_h = drawn % s.inner;
-      draw();
-      for (;; gb += 32) {
-        int nn, LL;
-        lane_seq(gb, nn, LL, false);
-        const int mine = (nn + s.BT - 1) / s.BT * s.H;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, gpre + incl > t);
-        if (m) {
-          const int src = __ffs(m) - 1;
-          b = gb + src;
-          const int q = t - gpre - __shfl_sync(0xffffffffu, incl - mine, src);
-          const int nb = __shfl_sync(0xffffffffu, mine, src) / s.H;
-          h = q / nb;
-          j = nb - 1 - q % nb;
-          break;
-        }
-        gpre += __shfl_sync(0xffffffffu, incl, 31);
+  // whole items: the next one drawn -> b, h, j; false when there is none
+  __device__ __forceinline__ bool next_whole() {
+    const int drawn = __shfl_sync(0xffffffffu, ticket, 0);
+    const int t = s.inner == 1 ? drawn : drawn / s.inner;
+    if (t >= items || drawn < 0) return false;
+    lane_h = s.inner == 1 ? 0 : drawn % s.inner;
+    draw();
+#pragma unroll 1
+    for (;; gb += 32) {
+      int nn, LL;
+      lane_seq(gb, nn, LL, false);
+      const int mine = blocks(nn) * s.H;
+      const int incl = (int)warp_prefix(mine);
+      const unsigned m = __ballot_sync(0xffffffffu, gpre + incl > t);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        b = gb + src;
+        const int q = t - gpre - __shfl_sync(0xffffffffu, incl - mine, src);
+        const int nb = __shfl_sync(0xffffffffu, mine, src) / s.H;
+        h = q / nb;
+        j = nb - 1 - (q - h * nb);
+        break;
       }
-      chunk_seq(s, b, c0, n, L);
-      const ChunkBlock k = chunk_block(s, n, L, j);
-      fill(g, k, 0, k.tiles);
-      return true;
+      gpre += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (left <= 0) return false;
-    const ChunkBlock k = chunk_block(s, n, L, j);
-    const int take = (int)min(left, (int64_t)(k.steps - off));
-    const int end = off + take;
-    fill(g, k, k.split ? 2 * off : off, k.split ? min(k.tiles, 2 * end) : end);
-    if (off > 0) {
-      g.part = 2 * (c * s.inner + lane_h);
-    } else if (end < k.steps) {
-      g.part = 2 * (c * s.inner + lane_h) + 1;
-      // CTAs whose runs start before the item's end: run r starts at floor(r total / nc)
-      const int64_t e = pos + k.steps;
-      const int last = (int)min((int64_t)nc - 1, (e * nc + total - 1) / total - 1);
-      g.nparts = last - c + 1;
-    }
-    left -= take;
-    off = end;
-    if (off == k.steps) {
-      pos += k.steps;
-      off = 0;
-      if (++j == (n + s.BT - 1) / s.BT) {
-        j = 0;
-        if (++h == s.H) {
-          h = 0;
-          n = 0;
-          while (left > 0 && n == 0 && ++b < s.B) chunk_seq(s, b, c0, n, L);
-          if (n == 0) left = 0;
-        }
-      }
-    }
+    chunk_seq(s, b, c0, n, L);
     return true;
   }
 
-  __device__ __forceinline__ void fill(ChunkSeg& g, const ChunkBlock& k, int i0, int i1) {
+  // The next piece; false when there is none.
+  __device__ __forceinline__ bool next(ChunkSeg& g) {
+    if (whole ? !next_whole() : left == 0) return false;
+    const ChunkBlock k = chunk_block(s, n, L, j);
+    const int from = whole ? 0 : off;
+    const int end = whole ? k.steps : (int)min((uint32_t)k.steps, off + left);
+    g.nparts = 0;
+    g.part = -1;
+    const int slot = 2 * (c * s.inner + lane_h);
+    if (from > 0) {
+      g.part = slot;
+    } else if (end < k.steps) {
+      g.part = slot + 1;
+      // the runs from this one on that start before the item's end
+      int before = 0;
+#pragma unroll 1
+      for (int r = threadIdx.x & 31; r < runs; r += 32) before += start(r) < pos + k.steps;
+      g.nparts = __reduce_add_sync(0xffffffffu, before) - c;
+    }
     g.valid = 1;
     g.row0 = c0 + k.t0;
     g.ntok = k.nt;
@@ -316,9 +314,28 @@ struct ChunkSched {
     g.L = L;
     g.na = k.na;
     g.bs = k.bs;
-    g.i0 = i0;
-    g.i1 = i1;
     g.split = k.split;
+    g.i0 = k.split ? 2 * from : from;
+    g.i1 = k.split ? min(k.tiles, 2 * end) : end;
+    g.once = k.nt == n;
+    if (!whole) {
+      left -= end - from;
+      off = end;
+      if (off == k.steps) {
+        pos += k.steps;
+        off = 0;
+        if (++j == blocks(n)) {
+          j = 0;
+          if (++h == s.H) {
+            h = 0;
+            n = 0;
+            while (left > 0 && n == 0 && ++b < s.B) chunk_seq(s, b, c0, n, L);
+            if (n == 0) left = 0;
+          }
+        }
+      }
+    }
+    return true;
   }
 };
 

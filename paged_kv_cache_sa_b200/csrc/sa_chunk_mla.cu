@@ -90,6 +90,7 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
   sched.init(a.shape, blockIdx.x, gridDim.x);
   const int ppt = kKeyTile >> a.page_shift;
   const int my_page = lane % ppt, my_sub = lane / ppt;
+  const uint64_t policy = tc::l2_normal();
   int it = 0;  // tiles loaded
   bool ok = true;
   for (int n = 0; ok; ++n) {
@@ -156,7 +157,7 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
         if (p0 >= 0 && my_sub < subs)
           tc::tma_2d(smem + kKeys + (2 * gr + my_sub) * kSlice +
                          ((uint32_t)my_page << a.page_shift) * 128,
-                     kmap, (2 * gr + my_sub) * 64, p0 << a.page_shift, &mi.full[gr]);
+                     kmap, (2 * gr + my_sub) * 64, p0 << a.page_shift, &mi.full[gr], policy);
       }
       p0 = p1;
       p1 = p2;
