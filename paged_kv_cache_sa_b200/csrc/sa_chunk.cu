@@ -343,10 +343,6 @@ __device__ __forceinline__ uint32_t below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1;
 }
 
-// Of every kPolyOf pairs of probabilities the last kPoly are computed on the FMA pipes: the 16
-// exponentials a cycle of an SM's special-function unit would take as long as both products.
-constexpr int kPolyOf = 4, kPoly = 0;
-
 // ---- softmax and epilogue of chain t (four warps, thread = row) --------------------------
 template <int D>
 __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem,
@@ -373,29 +369,35 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
     const bool any = __any_sync(0xffffffffu, real);
     const int s = real ? g.s0 + tk : 0x3FFFFFFF;  // its slot (padding rows: no mask, unused)
     float m = -INFINITY, l = 0.f;
+    // slots and pages that the block's rows together may see (window > 0)
+    const int win = a.shape.window, sink = a.shape.sink;
+    const int win_page = win > 0 ? max(0, g.s0 - win + 1) >> a.page_shift : 0;
+    const int sink_pages = (sink + (1 << a.page_shift) - 1) >> a.page_shift;
+    const uint64_t sl2 = tc::pair(a.scale_log2, a.scale_log2);
     for (int i = 0; i < mine; ++i) {
+      // all that the scores are not needed for comes before they are waited for
       const int ti = g.split ? 2 * i + t : i;
       const int key0 = tile_of(g, g.i0 + ti) * kKeyTile;
+      const int hi = s - key0, lo = win > 0 ? hi - win : -1, sk = sink - key0;
+      // some key of the tile is hidden from some row of the warp
+      const bool masked = __any_sync(
+          0xffffffffu, real && (hi < kKeyTile - 1 || (lo >= 0 && sk <= min(lo, kKeyTile - 1))));
+      // some row of V was not loaded or lies behind the sequence's end
+      const bool ragged =
+          (g.split || t == 0) &&
+          (key0 + kKeyTile > g.L ||
+           (win > 0 && (key0 < sink || (win_page << a.page_shift) > key0)));
       if (!tc::wait_warp(&mi.s_full[t], ns++ & 1, &mi.quit, status)) return;
       tc::fence_after();
-      // V rows that no page was loaded for, or that lie behind the sequence's end, would meet
-      // a probability of zero; they are zeroed because 0 * NaN is not
-      const int lo_row =
-          a.shape.window > 0 && key0 >= a.shape.sink
-              ? ((max(0, g.s0 - a.shape.window + 1) >> a.page_shift) << a.page_shift) - key0
-              : 0;
-      const bool ragged = key0 + kKeyTile > g.L || lo_row > 0 ||
-                          (a.shape.window > 0 && key0 < a.shape.sink);
-      if (ragged && (g.split || t == 0)) {
+      if (ragged) {
+        // such rows would meet a probability of zero; they are zeroed because 0 * NaN is not
+        // (only now: with this tile's scores there, what the stage held before has been read, so
+        // that the parity names this fill)
         const int x = g.it0 + v_pos(g.split, nt, ti);
         if (!tc::wait_warp(&mi.full[x % Y::kStages], (x / Y::kStages) & 1, &mi.quit, status))
           return;
         const int key = key0 + r, page = key >> a.page_shift;
-        const bool in_window =
-            a.shape.window == 0 ||
-            page >= (max(0, g.s0 - a.shape.window + 1) >> a.page_shift) ||
-            page < ((a.shape.sink + (1 << a.page_shift) - 1) >> a.page_shift);
-        if (key >= g.L || !in_window) {
+        if (key >= g.L || (page < win_page && page >= sink_pages)) {
           const uint32_t base = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes + r * 128;
 #pragma unroll
           for (int e = 0; e < Y::kHalves * 8; ++e)
@@ -409,11 +411,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
       if (any) {
         uint32_t x[128];
         tc::tmem_ld128(s_col, x);
-        const int hi = s - key0, lo = a.shape.window > 0 ? hi - a.shape.window : -1;
-        const int sk = a.shape.sink - key0;
-        // some key of the tile hidden from some row of the warp
-        if (__any_sync(0xffffffffu, real && (hi < kKeyTile - 1 ||
-                                             (lo >= 0 && sk <= min(lo, kKeyTile - 1))))) {
+        if (masked) {
 #pragma unroll
           for (int c0 = 0; c0 < 128; c0 += 32) {
             const uint32_t see =
@@ -450,7 +448,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        const uint64_t sl2 = tc::pair(a.scale_log2, a.scale_log2), off2 = tc::pair(off, off);
+        const uint64_t off2 = tc::pair(off, off);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 64) {
@@ -466,13 +464,9 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               float p0, p1;
-              if (c % kPolyOf >= kPolyOf - kPoly) {
-                tc::exp2_poly(y[c], p0, p1);
-              } else {
-                tc::unpair(y[c], p0, p1);
-                p0 = fast_exp2(p0);
-                p1 = fast_exp2(p1);
-              }
+              tc::unpair(y[c], p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
               y[c] = tc::pair(p0, p1);
               p[(b0 >> 1) + c] = pack_bf16(p0, p1);
             }

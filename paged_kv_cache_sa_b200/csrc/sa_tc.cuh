@@ -138,27 +138,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// 2^a and 2^b on the FMA pipes, for arguments below 128: y = n + f with n the nearest integer
-// (adding 1.5 * 2^23 leaves it in the low bits), 2^f by a cubic on [-1/2, 1/2] fitted to the
-// least relative error (7.5e-5, a twentieth of half a bf16 step), n added to the exponent.
-// Below 2^-126 the result is 0 (an exact one for masked scores).
-__device__ __forceinline__ void exp2_poly(uint64_t y, float& a, float& b) {
-  float ya, yb;
-  unpair(y, ya, yb);
-  y = pair(fmaxf(ya, -150.f), fmaxf(yb, -150.f));
-  const uint64_t magic = pair(12582912.f, 12582912.f);
-  const uint64_t t = add2(y, magic);
-  const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), y);
-  uint64_t p = fma2(f, pair(5.5171624e-2f, 5.5171624e-2f), pair(2.4261113e-1f, 2.4261113e-1f));
-  p = fma2(p, f, pair(6.9326097e-1f, 6.9326097e-1f));
-  p = fma2(p, f, pair(9.9992806e-1f, 9.9992806e-1f));
-  float ta, tb;
-  unpair(t, ta, tb);
-  unpair(p, a, b);
-  a = __int_as_float(max((int)((__float_as_uint(ta) << 23) + __float_as_uint(a)), 0));
-  b = __int_as_float(max((int)((__float_as_uint(tb) << 23) + __float_as_uint(b)), 0));
-}
-
 // Registers per thread of a warpgroup (four warps, all of them call it): the shares of a block
 // add up to no more than it was launched with.
 template <int N>
