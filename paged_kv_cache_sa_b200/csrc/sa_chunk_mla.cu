@@ -266,11 +266,15 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
     for (int c = 0; c < 32; ++c) l[c] = 0.f;
     bool none = true;  // no key seen yet in this piece
     for (int i = 0; i < nt; ++i, ++it) {
-      const int key0 = tile_of(g, g.i0 + i) * kKeyTile, key = key0 + r;
+      // all that the scores are not needed for comes before they are waited for
+      const int key = tile_of(g, g.i0 + i) * kKeyTile + r;
+      const bool stored = key < g.L && pages.wanted(key >> a.page_shift);
+      const bool seen = key <= s && (a.shape.window == 0 || key > s - a.shape.window ||
+                                     key < a.shape.sink);
+      const bool ragged = !__all_sync(0xffffffffu, stored);
       if (!tc::wait_warp(&mi.s_full, it & 1, &mi.quit, status)) return;
       tc::fence_after();
-      const bool stored = key < g.L && pages.wanted(key >> a.page_shift);
-      if (!__all_sync(0xffffffffu, stored)) {
+      if (ragged) {
         // rows without a loaded token would meet a probability of zero; 0 * NaN is not 0
         if (!stored) {
           const uint32_t base = smem + kKeys + 4 * t * kSlice + r * 128;
@@ -283,8 +287,6 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         }
         __syncwarp();
       }
-      const bool seen = key <= s && (a.shape.window == 0 || key > s - a.shape.window ||
-                                     key < a.shape.sink);
       // P with the maximum in use, in place of the scores, while the vote on it goes round
       float p[32];
       auto probabilities = [&](bool vote) {
