@@ -116,29 +116,30 @@ struct Loader {
     const int sink_pages = (a.shape.sink + (1 << shift) - 1) >> shift;
     // keys that no other CTA reads leave L2 first: what every call starts from stays in it
     const uint64_t policy = g.once ? l2_evict_first() : tc::l2_normal();
-    int p0 = -1, p1 = -1, p2 = -1;  // physical pages of tiles i, i + 1, i + 2 (-1: none)
+    // page of this lane in tile i, and whether it is there and seen by some row
+    auto wanted = [&](int i, int& lp) {
+      lp = tile_of(g, g.i0 + i) * ppt + my_page;
+      return my_half < Y::kHalves && lp <= last_page && (lp >= win_page || lp < sink_pages);
+    };
+    // page-table entries of tiles i, i + 1, i + 2, looked at only when their tile comes
+    int p0 = -1, p1 = -1, p2 = -1, lp;
     for (int i = -3; i < nt; ++i) {
-      int p3 = -1;
-      if (i + 3 < nt && my_half < Y::kHalves) {
-        const int lp = tile_of(g, g.i0 + i + 3) * ppt + my_page;
-        if (lp <= last_page && (lp >= win_page || lp < sink_pages)) {
-          p3 = row[lp];
-          if (p3 < 0 || p3 >= a.n_pool) {
-            if ((lp << shift) <= s_hi) report(a.shape.status, SA_ERR_DEVICE_CHECK);
-            p3 = -1;
-          }
-        }
-      }
+      const int p3 = i + 3 < nt && wanted(i + 3, lp) ? row[lp] : -1;
       if (i >= 0) {
         const int x = g.it0 + (V ? v_pos(g.split, nt, i) : k_pos(g.split, i));
         const int st = x % Y::kStages;
+        bool copy = wanted(i, lp);
+        if (copy && (p0 < 0 || p0 >= a.n_pool)) {
+          if ((lp << shift) <= s_hi) report(a.shape.status, SA_ERR_DEVICE_CHECK);
+          copy = false;
+        }
         if (x >= Y::kStages && !tc::wait_warp(&mi.empty[st], (x / Y::kStages - 1) & 1, &mi.quit,
                                               a.shape.status))
           return false;
-        const unsigned m = __ballot_sync(0xffffffffu, p0 >= 0);
+        const unsigned m = __ballot_sync(0xffffffffu, copy);
         if (lane == 0) mbar_arrive_expect_tx(&mi.full[st], __popc(m) * a.P * 128);
         __syncwarp();
-        if (p0 >= 0)
+        if (copy)
           tc::tma_2d(smem + Y::kRing + st * Y::kTileBytes + my_half * kHalfBytes +
                          ((uint32_t)my_page << shift) * 128,
                      map, my_half * 64, (p0 * a.Hkv + g.h) << shift, &mi.full[st], policy);
@@ -414,11 +415,12 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         if (masked) {
 #pragma unroll
           for (int c0 = 0; c0 < 128; c0 += 32) {
-            const uint32_t see =
-                below(hi + 1 - c0) & (~below(lo + 1 - c0) | below(sk - c0));
+            const uint32_t see = below(hi + 1 - c0) & (~below(lo + 1 - c0) | below(sk - c0));
+            if (__any_sync(0xffffffffu, ~see)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((see >> c) & 1)) x[c0 + c] = 0xFF800000u;  // -inf
+              for (int c = 0; c < 32; ++c)
+                if (!((see >> c) & 1)) x[c0 + c] = 0xFF800000u;  // -inf
+            }
           }
         }
         float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -527,6 +529,14 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         f0 *= inv;
         f1 *= inv;
       }
+      // the four rows that this lane's group of four writes together
+      int64_t to[4];
+      bool there[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        to[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
+        there[k] = __shfl_sync(0xffffffffu, real, (lane & ~3) + k);
+      }
 #pragma unroll 1
       for (int c0 = c_from; c0 < c_to; c0 += 32) {
         uint32_t o[32];
@@ -570,12 +580,10 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
                 }
               }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // row k of the four
-            const int64_t to = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
-            if (__shfl_sync(0xffffffffu, real, (lane & ~3) + k))
-              *reinterpret_cast<uint4*>(a.out + to * D + c0 + (lane & 3) * 8) =
+          for (int k = 0; k < 4; ++k)  // row k of the four
+            if (there[k])
+              *reinterpret_cast<uint4*>(a.out + to[k] * D + c0 + (lane & 3) * 8) =
                   make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-          }
         }
         __syncwarp();
       }
@@ -772,6 +780,7 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   a.shape.inner = 1;
   a.shape.BT = 2 * a.TB;
   a.shape.ST = a.TB;
+  a.shape.extra = 2;
   const int longest = 1 << 30;  // no sequence is longer
   a.shape.sink = c.sink < longest ? c.sink : longest;
   a.shape.window = c.window < longest ? c.window : longest;

@@ -7,11 +7,12 @@
 // of two when a block is short enough for its rows to fill one matrix tile only (the kernel
 // then works on two key tiles at a time).
 //
-// Long lists are cut: the steps of all items, laid end to end in (sequence, head, block)
-// order, are dealt to the CTAs in equal runs, so a CTA holds at most two cut pieces (the end
+// Long lists are cut: the costs of all items (their steps, and a few more for what a piece
+// takes to start and end), laid end to end in (sequence, head, block) order, are dealt to the
+// CTAs in equal runs, so a CTA holds at most two cut pieces (the end
 // of one item, the start of another), kept in workspace slots 2 c and 2 c + 1 of CTA c and
-// joined by a second kernel.  When there are at least four times as many steps per CTA as the longest
-// item has, nothing is cut: CTAs draw whole items from a counter, which keeps the CTAs on the
+// joined by a second kernel.  When there is at least four times as much to do per CTA as the longest
+// item takes, nothing is cut: CTAs draw whole items from a counter, which keeps the CTAs on the
 // same head and so on the same keys in L2, longest blocks of a head first.
 // With inner > 1 the head groups of one piece go to `inner` neighbouring CTAs at the same time
 // instead of one after the other: they read the same keys.
@@ -54,6 +55,7 @@ struct ChunkShape {
   int inner;       // head groups side by side: CTAs [inner w, inner w + inner) share run w
   int BT;          // tokens of a full block
   int ST;          // blocks of at most this many tokens walk two tiles a step
+  int extra;       // what a piece costs besides its steps, in steps
   int sink, window;
   int64_t cap;     // max_pages * P
   int32_t* status;
@@ -61,7 +63,7 @@ struct ChunkShape {
 };
 
 struct ChunkBlock {
-  int t0, nt, na, bs, tiles, split, steps;
+  int t0, nt, na, bs, tiles, split, steps, cost;
 };
 
 __device__ __forceinline__ ChunkBlock chunk_block(const ChunkShape& s, int n, int L, int j) {
@@ -79,6 +81,7 @@ __device__ __forceinline__ ChunkBlock chunk_block(const ChunkShape& s, int n, in
   k.tiles = k.na + hi / kKeyTile - k.bs + 1;
   k.split = k.nt <= s.ST;
   k.steps = k.split ? (k.tiles + 1) >> 1 : k.tiles;
+  k.cost = k.steps + s.extra;  // the extra ones come first
   return k;
 }
 
@@ -109,10 +112,10 @@ struct ChunkSched {
   int runs, c;           // runs that the CTAs could take, and this CTA's
   int lane_h;            // its head group (inner > 1)
   bool whole;
-  uint32_t total, left;  // steps of all items (cut list); of this run still to hand out
+  uint32_t total, left;  // cost of all items (cut list); of this run still to hand out
   uint32_t per, rem;     // total = per * runs + rem
-  uint32_t pos;          // steps before the current item
-  int b, h, j, off;      // the current item and how many of its steps are gone
+  uint32_t pos;          // cost before the current item
+  int b, h, j, off;      // the current item and how much of its cost is gone
   int n, L, c0;          // its sequence
   int items, ticket;     // whole items: count, and the next one drawn
   int gb, gpre;          // whole items: group of 32 sequences, items before it
@@ -130,8 +133,8 @@ struct ChunkSched {
     if (q < s.B && !chunk_seq(s, q, cc, nn, LL) && check) report(s.status, SA_ERR_DEVICE_CHECK);
   }
 
-  // steps of all blocks (one head) of this lane's sequence, and of its longest block
-  __device__ __forceinline__ uint32_t seq_steps(int nn, int LL, uint32_t& longest) {
+  // cost of all blocks (one head) of this lane's sequence, and of its longest block
+  __device__ __forceinline__ uint32_t seq_cost(int nn, int LL, uint32_t& longest) {
     const int lane = threadIdx.x & 31;
     const int nb = blocks(nn);
     uint32_t sum = 0, most = 0;
@@ -146,7 +149,7 @@ struct ChunkSched {
       uint32_t mx = 0;
 #pragma unroll 1
       for (int q = many ? lane : 0; q < nb1; q += 32) {
-        const uint32_t st = chunk_block(s, n1, L1, q).steps;
+        const uint32_t st = chunk_block(s, n1, L1, q).cost;
         t += st;
         mx = max(mx, st);
       }
@@ -164,7 +167,7 @@ struct ChunkSched {
     return sum;
   }
 
-  // step that run r starts at, floor(r total / runs), for r <= runs
+  // where run r starts, floor(r total / runs), for r <= runs
   __device__ __forceinline__ uint32_t start(uint32_t r) const { return r * per + r * rem / runs; }
 
   __device__ __forceinline__ void init(const ChunkShape& shape, int cta, int n_cta) {
@@ -181,7 +184,7 @@ struct ChunkSched {
       int nn, LL;
       uint32_t mx;
       lane_seq(base, nn, LL, cta == 0);
-      mine = seq_steps(nn, LL, mx);
+      mine = seq_cost(nn, LL, mx);
       all += __reduce_add_sync(0xffffffffu, mine & 0xFFFFu) +
              ((uint64_t)__reduce_add_sync(0xffffffffu, mine >> 16) << 16);
       items += __reduce_add_sync(0xffffffffu, blocks(nn));
@@ -209,7 +212,7 @@ struct ChunkSched {
     if (c >= runs) return;
     const uint32_t x0 = start(c);
     left = start(c + 1) - x0;
-    // the sequence and head that step x0 belongs to
+    // the sequence and head that x0 lies in
     pos = 0;
 #pragma unroll 1
     for (int base = 0;; base += 32) {
@@ -217,7 +220,7 @@ struct ChunkSched {
         int nn, LL;
         uint32_t mx;
         lane_seq(base, nn, LL, false);
-        mine = seq_steps(nn, LL, mx);
+        mine = seq_cost(nn, LL, mx);
       }
       const uint32_t incl = warp_prefix(mine * s.H);
       const unsigned m = __ballot_sync(0xffffffffu, pos + incl > x0);
@@ -238,7 +241,7 @@ struct ChunkSched {
     if (nb > 1) {
 #pragma unroll 1
       for (;; j += 32) {
-        const uint32_t st = j + lane < nb ? chunk_block(s, n, L, j + lane).steps : 0;
+        const uint32_t st = j + lane < nb ? chunk_block(s, n, L, j + lane).cost : 0;
         const uint32_t incl = warp_prefix(st);
         const unsigned m = __ballot_sync(0xffffffffu, pos + incl > x0);
         if (m) {
@@ -290,8 +293,15 @@ struct ChunkSched {
   __device__ __forceinline__ bool next(ChunkSeg& g) {
     if (whole ? !next_whole() : left == 0) return false;
     const ChunkBlock k = chunk_block(s, n, L, j);
-    const int from = whole ? 0 : off;
-    const int end = whole ? k.steps : (int)min((uint32_t)k.steps, off + left);
+    int from = 0, end = k.steps;  // the piece, in steps
+    if (!whole) {
+      const int stop = (int)min((uint32_t)k.cost, off + left);
+      from = max(off - s.extra, 0);
+      end = max(stop - s.extra, 0);
+      left -= stop - off;
+      off = stop;
+      if (end == 0) return false;  // the run ends before the item's first step
+    }
     g.nparts = 0;
     g.part = -1;
     const int slot = 2 * (c * s.inner + lane_h);
@@ -302,7 +312,7 @@ struct ChunkSched {
       // the runs from this one on that start before the item's end
       int before = 0;
 #pragma unroll 1
-      for (int r = threadIdx.x & 31; r < runs; r += 32) before += start(r) < pos + k.steps;
+      for (int r = threadIdx.x & 31; r < runs; r += 32) before += start(r) < pos + k.cost;
       g.nparts = __reduce_add_sync(0xffffffffu, before) - c;
     }
     g.valid = 1;
@@ -318,20 +328,16 @@ struct ChunkSched {
     g.i0 = k.split ? 2 * from : from;
     g.i1 = k.split ? min(k.tiles, 2 * end) : end;
     g.once = k.nt == n;
-    if (!whole) {
-      left -= end - from;
-      off = end;
-      if (off == k.steps) {
-        pos += k.steps;
-        off = 0;
-        if (++j == blocks(n)) {
-          j = 0;
-          if (++h == s.H) {
-            h = 0;
-            n = 0;
-            while (left > 0 && n == 0 && ++b < s.B) chunk_seq(s, b, c0, n, L);
-            if (n == 0) left = 0;
-          }
+    if (!whole && off == k.cost) {
+      pos += k.cost;
+      off = 0;
+      if (++j == blocks(n)) {
+        j = 0;
+        if (++h == s.H) {
+          h = 0;
+          n = 0;
+          while (left > 0 && n == 0 && ++b < s.B) chunk_seq(s, b, c0, n, L);
+          if (n == 0) left = 0;
         }
       }
     }

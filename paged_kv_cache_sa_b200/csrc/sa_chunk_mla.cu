@@ -561,6 +561,7 @@ cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t 
   a.shape.inner = 2;
   a.shape.BT = 1;
   a.shape.ST = 0;
+  a.shape.extra = 2;
   const int longest = 1 << 30;  // no sequence is longer
   a.shape.sink = c.sink < longest ? c.sink : longest;
   a.shape.window = c.window < longest ? c.window : longest;
