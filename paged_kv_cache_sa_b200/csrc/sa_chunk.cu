@@ -36,6 +36,9 @@ constexpr int kThreads = 384;
 // registers: 168 a thread at launch (384 x 168 = 64512); 256 x 208 + 128 x 88 = 64512
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kSegs = 2;
+// probabilities are handed over in two parts, so that the product over the first keys runs while
+// the last ones are computed (2% of a long chunk against 64 + 64)
+constexpr int kFirstKeys = 96;
 constexpr uint32_t kHalfBytes = kKeyTile * 128;  // 128 rows of 64 channels
 
 template <int D>
@@ -54,7 +57,7 @@ struct Misc {
   ChunkSeg seg[kSegs];
   uint64_t full[10], empty[10];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full, q_empty, s_full[2], p_half[2], p_full[2], o_full[2], meet, drain;
+  uint64_t q_full, q_empty, s_full[2], p_part[2], p_full[2], o_full[2], meet, drain;
   uint32_t tmem;
   int quit;
 };
@@ -242,18 +245,18 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
     }
     tc::commit(&mi.s_full[t]);
   };
-  // O_t += P_t V of stage x, as the halves of P_t come; `then` follows in the same lane
+  // O_t += P_t V of stage x, as the two parts of P_t come; `then` follows in the same lane
   auto values = [&](int t, int x, bool first, auto then) -> bool {
     const uint32_t v = smem + Y::kRing + (x % Y::kStages) * Y::kTileBytes;
     const uint32_t parity = np[t]++ & 1;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      if (!tc::wait_warp(hf ? &mi.p_full[t] : &mi.p_half[t], parity, &mi.quit, status))
+      if (!tc::wait_warp(hf ? &mi.p_full[t] : &mi.p_part[t], parity, &mi.quit, status))
         return false;
       tc::fence_after();
       if (tc::elect()) {
 #pragma unroll
-        for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
+        for (int kk = hf ? kFirstKeys / 16 : 0; kk < (hf ? kKeyTile : kFirstKeys) / 16; ++kk)
           tc::mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8,
                      tc::desc(v + kk * 2048, kHalfBytes), id_o, !(first && kk == 0));
         if (hf) then();
@@ -416,11 +419,9 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
 #pragma unroll
           for (int c0 = 0; c0 < 128; c0 += 32) {
             const uint32_t see = below(hi + 1 - c0) & (~below(lo + 1 - c0) | below(sk - c0));
-            if (__any_sync(0xffffffffu, ~see)) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!((see >> c) & 1)) x[c0 + c] = 0xFF800000u;  // -inf
-            }
+            for (int c = 0; c < 32; ++c)
+              if (!((see >> c) & 1)) x[c0 + c] = 0xFF800000u;  // -inf
           }
         }
         float mxs[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -453,34 +454,31 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         const uint64_t off2 = tc::pair(off, off);
         uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
-          uint32_t p[32];
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint64_t y[16];
+          uint32_t p[16];
 #pragma unroll
-          for (int b0 = 0; b0 < 64; b0 += 32) {
-            uint64_t y[16];
+          for (int c = 0; c < 16; ++c)
+            y[c] = tc::fma2(tc::pair(__uint_as_float(x[c0 + 2 * c]),
+                                     __uint_as_float(x[c0 + 2 * c + 1])),
+                            sl2, off2);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              y[c] = tc::fma2(tc::pair(__uint_as_float(x[c0 + b0 + 2 * c]),
-                                       __uint_as_float(x[c0 + b0 + 2 * c + 1])),
-                              sl2, off2);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float p0, p1;
-              tc::unpair(y[c], p0, p1);
-              p0 = fast_exp2(p0);
-              p1 = fast_exp2(p1);
-              y[c] = tc::pair(p0, p1);
-              p[(b0 >> 1) + c] = pack_bf16(p0, p1);
-            }
-#pragma unroll
-            for (int c = 0; c < 16; ++c) sum[c & 1] = tc::add2(sum[c & 1], y[c]);
+          for (int c = 0; c < 16; ++c) {
+            float p0, p1;
+            tc::unpair(y[c], p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            y[c] = tc::pair(p0, p1);
+            p[c] = pack_bf16(p0, p1);
           }
-          tc::tmem_st32(s_col + (c0 >> 1), p);
-          if (c0 == 0) {  // the product over the first 64 keys may start
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sum[c & 1] = tc::add2(sum[c & 1], y[c]);
+          tc::tmem_st16(s_col + (c0 >> 1), p);
+          if (c0 + 32 == kFirstKeys) {  // the product over the first keys may start
             tc::tmem_wait_st();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&mi.p_half[t]);
+            if (lane == 0) mbar_arrive(&mi.p_part[t]);
           }
         }
         float a0, a1, a2, a3;
@@ -489,7 +487,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         l += (a0 + a1) + (a2 + a3);
         tc::tmem_wait_st();
       } else if (lane == 0) {
-        mbar_arrive(&mi.p_half[t]);
+        mbar_arrive(&mi.p_part[t]);
       }
       tc::fence_before();
       __syncwarp();
@@ -528,14 +526,6 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         const float inv = l > 0.f ? 1.f / l : 0.f;
         f0 *= inv;
         f1 *= inv;
-      }
-      // the four rows that this lane's group of four writes together
-      int64_t to[4];
-      bool there[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        to[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
-        there[k] = __shfl_sync(0xffffffffu, real, (lane & ~3) + k);
       }
 #pragma unroll 1
       for (int c0 = c_from; c0 < c_to; c0 += 32) {
@@ -580,10 +570,12 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
                 }
               }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // row k of the four
-            if (there[k])
-              *reinterpret_cast<uint4*>(a.out + to[k] * D + c0 + (lane & 3) * 8) =
+          for (int k = 0; k < 4; ++k) {  // row k of the four
+            const int64_t to = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
+            if (__shfl_sync(0xffffffffu, real, (lane & ~3) + k))
+              *reinterpret_cast<uint4*>(a.out + to * D + c0 + (lane & 3) * 8) =
                   make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+          }
         }
         __syncwarp();
       }
@@ -632,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mi.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&mi.s_full[t], 1);
-      mbar_init(&mi.p_half[t], 4);
+      mbar_init(&mi.p_part[t], 4);
       mbar_init(&mi.p_full[t], 4);
       mbar_init(&mi.o_full[t], 1);
     }
