@@ -15,7 +15,8 @@
 // item takes, nothing is cut: CTAs draw whole items from a counter, which keeps the CTAs on the
 // same head and so on the same keys in L2, longest blocks of a head first.
 // With inner > 1 the head groups of one piece go to `inner` neighbouring CTAs at the same time
-// instead of one after the other: they read the same keys.
+// instead of one after the other: they read the same keys.  Such CTAs make the same list, so
+// whole items go round in turn there, not by the counter.
 #pragma once
 
 #include "sa_common.cuh"
@@ -59,7 +60,7 @@ struct ChunkShape {
   int sink, window;
   int64_t cap;     // max_pages * P
   int32_t* status;
-  int32_t* ticket;  // header word, zero between calls
+  int32_t* ticket;  // header word, zero between calls; NULL: whole items go round in turn
 };
 
 struct ChunkBlock {
@@ -202,6 +203,7 @@ struct ChunkSched {
     if (whole) {
       gb = 0;
       gpre = 0;
+      ticket = c - runs;
       draw();
       return;
     }
@@ -257,15 +259,16 @@ struct ChunkSched {
   }
 
   __device__ __forceinline__ void draw() {
-    if ((threadIdx.x & 31) == 0) ticket = atomicAdd(s.ticket, 1);
+    if (!s.ticket)
+      ticket += runs;
+    else if ((threadIdx.x & 31) == 0)
+      ticket = atomicAdd(s.ticket, 1);
   }
 
   // whole items: the next one drawn -> b, h, j; false when there is none
   __device__ __forceinline__ bool next_whole() {
-    const int drawn = __shfl_sync(0xffffffffu, ticket, 0);
-    const int t = s.inner == 1 ? drawn : drawn / s.inner;
-    if (t >= items || drawn < 0) return false;
-    lane_h = s.inner == 1 ? 0 : drawn % s.inner;
+    const int t = __shfl_sync(0xffffffffu, ticket, 0);
+    if (t >= items || t < 0) return false;
     draw();
 #pragma unroll 1
     for (;; gb += 32) {

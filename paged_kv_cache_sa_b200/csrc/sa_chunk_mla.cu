@@ -2,21 +2,22 @@
 // latent geometry (128 query heads share one 576-wide key per token, V its first 512
 // channels), on the 5th-generation tensor cores.
 //
-// Method: as sa_chunk.cu, with both products transposed.  An accumulator of 128 heads by 512
-// channels would fill tensor memory and leave no place for scores; so a CTA takes 64 heads
-// of one token (a neighbouring CTA the other 64, reading the same keys at the same time):
-//   S^T = K Q^T   (128 keys x 64 heads, K = 576 channels, keys K-major)
-//   O^T += V^T P^T (four blocks of 128 channels x 64 heads, K = 128 keys, keys MN-major)
-// which is 64 + 256 columns.  Both products read the keys from the same place in shared
-// memory: a tile's nine slices of 64 channels are loaded once (144 KB; with the queries'
-// 72 KB all that fits), P^T overwrites the ninth slice (the rotated channels, not part of
-// V) once the scores are done, and the loads of the next tile follow the products of this
-// one slice pair by slice pair.  The next tiles' pages are asked into L2 ahead of that.
-// Softmax: a thread has one key and 32 of the heads, so a maximum over keys crosses threads.
-// It is only taken when some score exceeds the maximum in use by more than 2^8 (which a vote
+// Method: as sa_chunk.cu.  A tile is one token's 128 heads against 128 keys, worked on by a pair
+// of CTAs (cta_group::2): each CTA has 64 of the heads as its rows, so that
+//   S = Q K^T     (128 x 128 x 576)  takes 64 columns of its tensor memory,
+//   O += P V      (128 x 512 x 128)  takes 256,
+// and two score tiles fit beside the accumulator; one CTA alone would need all 512 columns for
+// O.  (Alone, with 64 heads a CTA and both products transposed, every product has N = 64 and
+// takes as long as one with N = 128: 1.60 ms instead of TIME for 256 + 100 rows at 16K / 5K.)
+// Of a key tile a CTA loads what its half of the products reads: 64 keys of all 576 channels
+// as B of the first (72 KB), 256 channels of all 128 keys as B of the second (64 KB), with
+// 72 KB of queries and 16 KB of probabilities.  The next tile's keys come in while this one's
+// softmax and second product run, the next values during the next scores.
+// A thread has one row and 32 of its 128 scores, so a row's maximum crosses four threads.  It
+// is only taken when some score exceeds the maximum in use by more than 2^8 (which a vote
 // finds); sums stay in the threads until the end.
-// Warps 0-3 and 4-7: softmax of heads 0-31 and 32-63; 8: issues the products; 9: work list
-// and TMA.
+// Warps 0-3 and 4-7: softmax; 8: issues the products (even CTA); 9: work list, queries and
+// keys; 10: values; 8 and 11 of the odd CTA: tell the even one what has been loaded.
 #include "sa_chunk.cuh"
 #include "sa_internal.h"
 #include "sa_tc.cuh"
@@ -26,28 +27,27 @@ namespace sa {
 namespace chunk_mla {
 
 constexpr int kD = 576, kDv = 512, kHeads = 128;
-constexpr int kHalf = 64;  // heads of a CTA
-constexpr int kThreads = 320;
+constexpr int kHalf = 64;  // heads of a CTA, and keys that it loads for the scores
+constexpr int kThreads = 384;
 constexpr int kSegs = 2;
-constexpr int kGroups = 5;  // slice pairs 0-1, 2-3, 4-5, 6-7 and slice 8
-constexpr uint32_t kSlice = kKeyTile * 128;
-constexpr uint32_t kQSlice = kHalf * 128;
-constexpr uint32_t kKeys = 9 * kQSlice;  // queries first
-constexpr uint32_t kMisc = kKeys + 9 * kSlice;
-constexpr uint32_t kP = kKeys + 8 * kSlice;
-constexpr uint32_t kO = 64;  // column of O^T; S^T is columns 0-63
+constexpr uint32_t kQSlice = kHalf * 128;     // 64 rows of 64 channels
+constexpr uint32_t kVSlice = kKeyTile * 128;  // 128 keys' 64 channels
+constexpr uint32_t kKeys = 9 * kQSlice;       // queries first
+constexpr uint32_t kValues = 2 * 9 * kQSlice;
+constexpr uint32_t kP = kValues + 4 * kVSlice;  // [2 key halves][64 rows][64 keys]
+constexpr uint32_t kMisc = kP + 2 * kQSlice;
+constexpr uint32_t kO = 128;  // column of O; the two score tiles are columns 0-63 and 64-127
 
 struct Misc {
-  float off[2][32];  // minus the maximum in use of every head (0 while there is none)
-  float fac[2][32];  // rescaling factors, then 1 / l
-  float red[2][4][32];
+  float red[4][64];  // of a row's four threads
   ChunkSeg seg[kSegs];
-  uint64_t full[kGroups], empty[kGroups];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full, q_empty, s_full, p_full, o_full, drain, meet[2];
+  uint64_t q_full, k_full, v_full;     // this CTA's loads
+  uint64_t q_peer, k_peer, v_peer;     // the other's (at the even CTA)
+  uint64_t q_empty, k_empty, s_full[2], p_full, o_done, drain, meet;
   uint32_t tmem;
   int quit;
-  int vote[2][3];
+  int vote[3];
 };
 constexpr uint32_t kSmem = kMisc + sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -58,7 +58,7 @@ struct Args {
   const uint8_t* kv;
   uint16_t* out;
   float* lse;
-  float* part_o;    // [2 n_cta][512 channels][64 heads]
+  float* part_o;    // [2 n_cta][512 / 4 channels][64 heads][4]
   float2* part_ml;  // [2 n_cta][64]
   ChunkCut* cut;    // [n_cta]
   int P, page_shift, max_pages, n_pool;
@@ -81,25 +81,82 @@ struct Pages {
   }
 };
 
-__device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
-                                        const CUtensorMap* qmap, const CUtensorMap* kmap) {
+// Copies of one piece's tiles.  V: 256 channels of all keys (a lane: slice lane % 4, pages
+// lane / 4, + 8, ...), else 64 keys of all channels (a lane: slices lane % 9 of page lane / 9,
+// in as many rounds as it takes).  `it`: tiles before the piece; `free`: completes once per tile.
+template <bool V>
+__device__ __forceinline__ bool load_tiles(const Args& a, uint32_t smem, Misc& mi,
+                                           const ChunkSeg& g, const CUtensorMap* map, int it,
+                                           uint32_t rank) {
+  const int lane = threadIdx.x & 31, shift = a.page_shift;
+  const int ppt = kKeyTile >> shift, mine = V ? ppt : ppt >> 1;  // pages of a tile; of this copy
+  const int nt = g.i1 - g.i0, last_page = (g.L - 1) >> shift;
+  const Pages pages(a, g);
+  const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
+  const uint64_t policy = tc::l2_normal();
+  uint64_t* full = V ? &mi.v_full : &mi.k_full;
+  uint64_t* empty = V ? &mi.o_done : &mi.k_empty;
+  // lane p < mine looks up page p of the copy, two tiles ahead; entries are checked when used
+  auto wanted = [&](int i, int& lp) {
+    lp = tile_of(g, g.i0 + i) * ppt + (V ? 0 : (int)rank * mine) + lane;
+    return lane < mine && lp <= last_page && pages.wanted(lp);
+  };
+  int p0 = -1, p1 = -1, lp;
+  for (int i = -2; i < nt; ++i) {
+    int p2 = -1;
+    if (i + 2 < nt && wanted(i + 2, lp)) {
+      p2 = row[lp];
+      if (!V && p2 >= 0 && p2 < a.n_pool)  // ask the page into L2
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         a.kv + (size_t)p2 * a.P * (kD * 2)),
+                     "r"(a.P * (kD * 2))
+                     : "memory");
+    }
+    if (i >= 0) {
+      bool copy = wanted(i, lp);
+      if (copy && (p0 < 0 || p0 >= a.n_pool)) {
+        if ((lp << shift) <= g.s0) report(a.shape.status, SA_ERR_DEVICE_CHECK);
+        copy = false;
+      }
+      const unsigned have = __ballot_sync(0xffffffffu, copy);
+      if (it + i > 0 &&
+          !tc::wait_warp(empty, (it + i - 1) & 1, &mi.quit, a.shape.status))
+        return false;
+      constexpr int kSlices = V ? 4 : 9;
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * kSlices * a.P * 128);
+      __syncwarp();
+      for (int e0 = 0; e0 < mine * kSlices; e0 += 32) {
+        const int e = e0 + lane, pg = min(e / kSlices, mine - 1), sl = e % kSlices;
+        const int ph = __shfl_sync(0xffffffffu, p0, pg);
+        if (e < mine * kSlices && ((have >> pg) & 1)) {
+          // V: slices 0, 1 are channels 128 rank .. of the first 256, 2, 3 of the others
+          const int ch = V ? (sl >> 1) * 256 + (int)rank * 128 + (sl & 1) * 64 : sl * 64;
+          tc::tma_2d(smem + (V ? kValues + sl * kVSlice : kKeys + sl * kQSlice) +
+                         ((uint32_t)pg << shift) * 128,
+                     map, ch, ph << shift, full, policy);
+        }
+      }
+    }
+    p0 = p1;
+    p1 = p2;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void produce_k(const Args& a, uint32_t smem, Misc& mi,
+                                          const CUtensorMap* qmap, const CUtensorMap* kmap,
+                                          uint32_t rank) {
   const int lane = threadIdx.x & 31;
   int32_t* status = a.shape.status;
   ChunkSched sched;
   if (lane == 0) a.cut[blockIdx.x].nparts = 0;
   sched.init(a.shape, blockIdx.x, gridDim.x);
-  const int ppt = kKeyTile >> a.page_shift;
-  const int my_page = lane % ppt, my_sub = lane / ppt;
-  const uint64_t policy = tc::l2_normal();
   int it = 0;  // tiles loaded
-  bool ok = true;
-  for (int n = 0; ok; ++n) {
+  for (int n = 0;; ++n) {
     const int slot = n % kSegs;
     if (n >= kSegs &&
-        !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit, status)) {
-      ok = false;
+        !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit, status))
       break;
-    }
     ChunkSeg g;
     const bool more = sched.next(g);
     if (!more) g.valid = 0;
@@ -109,436 +166,416 @@ __device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
       mbar_arrive(&mi.seg_full[slot]);
       if (more && g.nparts > 0) a.cut[blockIdx.x] = ChunkCut{g.nparts, g.row0, g.ntok, g.h};
     }
-    if (!more) break;
-    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, status)) {
-      ok = false;
-      break;
-    }
+    if (!more) return;
+    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, status)) break;
     if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, 9 * kQSlice);
     __syncwarp();
     if (lane < 9)
       tc::tma_3d(smem + lane * kQSlice, qmap, lane * 64, g.h * kHalf, g.row0, &mi.q_full);
-    const int nt = g.i1 - g.i0;
-    const int last_page = (g.L - 1) >> a.page_shift;
-    const Pages pages(a, g);
-    const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
-    auto lookup = [&](int i) -> int {
-      if (i >= nt) return -1;
-      const int lp = tile_of(g, g.i0 + i) * ppt + my_page;
-      if (my_sub > 1 || lp > last_page || !pages.wanted(lp)) return -1;
-      const int ph = row[lp];
-      if (ph < 0 || ph >= a.n_pool) {
-        if ((lp << a.page_shift) <= g.s0) report(status, SA_ERR_DEVICE_CHECK);
-        return -1;
-      }
-      return ph;
-    };
-    auto ask = [&](int ph) {  // a page into L2
-      if (ph >= 0 && my_sub == 0)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                         a.kv + (size_t)ph * a.P * (kD * 2)),
-                     "r"(a.P * (kD * 2))
-                     : "memory");
-    };
-    int p0 = lookup(0), p1 = lookup(1), p2 = lookup(2);
-    ask(p1);
-    for (int i = 0; i < nt && ok; ++i, ++it) {
-      const int p3 = lookup(i + 3);
-      ask(p2);
-      const unsigned m = __ballot_sync(0xffffffffu, p0 >= 0 && my_sub == 0);
-      for (int gr = 0; gr < kGroups; ++gr) {
-        if (it > 0 && !tc::wait_warp(&mi.empty[gr], (it - 1) & 1, &mi.quit, status)) {
-          ok = false;
-          break;
-        }
-        const int subs = gr == 4 ? 1 : 2;
-        if (lane == 0) mbar_arrive_expect_tx(&mi.full[gr], subs * __popc(m) * a.P * 128);
-        __syncwarp();
-        if (p0 >= 0 && my_sub < subs)
-          tc::tma_2d(smem + kKeys + (2 * gr + my_sub) * kSlice +
-                         ((uint32_t)my_page << a.page_shift) * 128,
-                     kmap, (2 * gr + my_sub) * 64, p0 << a.page_shift, &mi.full[gr], policy);
-      }
-      p0 = p1;
-      p1 = p2;
-      p2 = p3;
-    }
+    if (!load_tiles<false>(a, smem, mi, g, kmap, it, rank)) break;
+    it += g.i1 - g.i0;
   }
-  if (!ok) {  // given up: let copies in flight land (bounded) before shared memory goes away
-    for (int gr = 0; gr < kGroups; ++gr)
-      for (int x = max(0, it - 1); x <= it; ++x) mbar_wait(&mi.full[gr], x & 1);
+  // given up: copies in flight land (bounded) before shared memory goes away
+  for (int ph = 0; ph < 2; ++ph) {
+    mbar_wait(&mi.k_full, ph);
+    mbar_wait(&mi.q_full, ph);
   }
 }
 
+// Reads the list as the other warps do: the next piece, or false.
+__device__ __forceinline__ bool next_piece(Misc& mi, int n, int32_t* status, ChunkSeg& g) {
+  const int slot = n % kSegs;
+  if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return false;
+  g = mi.seg[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&mi.seg_empty[slot]);
+  return g.valid != 0;
+}
+
+__device__ __forceinline__ void produce_v(const Args& a, uint32_t smem, Misc& mi,
+                                          const CUtensorMap* kmap, uint32_t rank) {
+  ChunkSeg g;
+  for (int n = 0; next_piece(mi, n, a.shape.status, g); ++n)
+    if (!load_tiles<true>(a, smem, mi, g, kmap, g.it0, rank)) break;
+  if (*(volatile int*)&mi.quit)
+    for (int ph = 0; ph < 2; ++ph) mbar_wait(&mi.v_full, ph);
+}
+
+// The odd CTA: passes on that its queries and keys (its values) have come.
+template <bool V>
+__device__ __forceinline__ void forward(const Args& a, Misc& mi) {
+  const bool one = (threadIdx.x & 31) == 0;
+  int32_t* status = a.shape.status;
+  ChunkSeg g;
+  for (int n = 0; next_piece(mi, n, status, g); ++n) {
+    if (!V) {
+      if (!tc::wait_warp(&mi.q_full, n & 1, &mi.quit, status)) return;
+      if (one) tc::arrive_at_first(&mi.q_peer);
+    }
+    for (int it = g.it0; it < g.it0 + g.i1 - g.i0; ++it) {
+      if (!tc::wait_warp(V ? &mi.v_full : &mi.k_full, it & 1, &mi.quit, status)) return;
+      if (one) tc::arrive_at_first(V ? &mi.v_peer : &mi.k_peer);
+    }
+  }
+}
+
+// The even CTA: all products.
 __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem) {
-  constexpr uint32_t id_s = tc::idesc(kKeyTile, kHalf, false, false);
-  constexpr uint32_t id_o = tc::idesc(128, kHalf, true, true);
+  constexpr uint32_t id_s = tc::idesc(128, kKeyTile, false, false);
+  constexpr uint32_t id_o = tc::idesc(128, 256, false, true);
   int32_t* status = a.shape.status;
   int it = 0;
-  for (int n = 0;; ++n) {
-    const int slot = n % kSegs;
-    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
-    const int nt = __shfl_sync(0xffffffffu, mi.seg[slot].i1 - mi.seg[slot].i0, 0);
-    const bool valid = __shfl_sync(0xffffffffu, mi.seg[slot].valid, 0) != 0;
-    if (tc::elect()) mbar_arrive(&mi.seg_empty[slot]);
-    if (!valid) return;
-    if (!tc::wait_warp(&mi.q_full, n & 1, &mi.quit, status)) return;
-    for (int i = 0; i < nt; ++i, ++it) {
+  auto both = [&](uint64_t* own, uint64_t* peer, uint32_t parity) {
+    return tc::wait_warp(own, parity & 1, &mi.quit, status) &&
+           tc::wait_cluster_warp(peer, parity & 1, &mi.quit, status);
+  };
+  auto scores = [&](int x, bool last) -> bool {  // S of tile x
+    if (!both(&mi.k_full, &mi.k_peer, x)) return false;
+    tc::fence_after();
+    if (tc::elect()) {
 #pragma unroll
-      for (int gr = 0; gr < kGroups; ++gr) {
-        if (!tc::wait_warp(&mi.full[gr], it & 1, &mi.quit, status)) return;
-        tc::fence_after();
-        if (tc::elect()) {
-#pragma unroll
-          for (int kk = 0; kk < (gr == 4 ? 4 : 8); ++kk) {
-            const int sl = 2 * gr + (kk >> 2);
-            tc::mma_ss(tmem, tc::desc(smem + kKeys + sl * kSlice + (kk & 3) * 32),
-                       tc::desc(smem + sl * kQSlice + (kk & 3) * 32), id_s, gr + kk != 0);
-          }
-          if (gr == 4) {
-            tc::commit(&mi.s_full);
-            if (i + 1 == nt) tc::commit(&mi.q_empty);
-          }
-        }
-        __syncwarp();
+      for (int kk = 0; kk < kD / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * kQSlice + (kk & 3) * 32;
+        tc::pair_mma(tmem + (x & 1) * 64, tc::desc(smem + o), tc::desc(smem + kKeys + o), id_s,
+                     kk != 0);
       }
-      if (!tc::wait_warp(&mi.p_full, it & 1, &mi.quit, status)) return;
+      tc::pair_commit(&mi.s_full[x & 1]);
+      tc::pair_commit(&mi.k_empty);
+      if (last) tc::pair_commit(&mi.q_empty);
+    }
+    __syncwarp();
+    return true;
+  };
+  for (int n = 0;; ++n) {
+    ChunkSeg g;
+    if (!next_piece(mi, n, status, g)) return;
+    const int nt = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
+    if (!both(&mi.q_full, &mi.q_peer, n) || !scores(it, nt == 1)) return;
+    for (int i = 0; i < nt; ++i, ++it) {
+      if (i + 1 < nt && !scores(it + 1, i + 2 == nt)) return;
+      if (!both(&mi.v_full, &mi.v_peer, it) ||
+          !tc::wait_cluster_warp(&mi.p_full, it & 1, &mi.quit, status))
+        return;
       tc::fence_after();
       if (tc::elect()) {
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
+        for (int kk = 0; kk < kKeyTile / 16; ++kk)
 #pragma unroll
-          for (int kk = 0; kk < kKeyTile / 16; ++kk)
-            tc::mma_ss(tmem + kO + cb * 64,
-                       tc::desc(smem + kKeys + 2 * cb * kSlice + kk * 2048, kSlice),
-                       tc::desc(smem + kP + kk * 2048), id_o, !(i == 0 && kk == 0));
-          tc::commit(&mi.empty[cb]);
-        }
-        tc::commit(&mi.empty[4]);
-        if (i + 1 == nt) tc::commit(&mi.o_full);
+          for (int cb = 0; cb < 2; ++cb)
+            tc::pair_mma(tmem + kO + cb * 128,
+                         tc::desc(smem + kP + (kk >> 2) * kQSlice + (kk & 3) * 32),
+                         tc::desc(smem + kValues + 2 * cb * kVSlice + kk * 2048, kVSlice), id_o,
+                         !(i == 0 && kk == 0));
+        tc::pair_commit(&mi.o_done);
       }
       __syncwarp();
     }
   }
 }
 
-// v[c] of every lane combined over the warp: lane c gets column c
-template <bool MAX>
-__device__ __forceinline__ float across(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, o);
-      v[i] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return v[0];
-}
-
-// softmax and epilogue of heads [32 t, 32 t + 32) of the CTA's 64
+// softmax and epilogue: columns [32 t, 32 t + 32) of a score tile's 64, accumulator block t
 __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem,
-                                       int t) {
+                                       int t, uint32_t rank) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3;
-  const int r = wq * 32 + lane;  // key of the tile; channel of a block of O^T
+  const int l128 = wq * 32 + lane;                   // lane of tensor memory
+  const int row = l128 & 63, second = l128 >> 6;     // head of the CTA; half of the columns
   const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+  const int key_in = second * 64 + t * 32;           // first key of this thread in a tile
+  const uint32_t p_row = smem + kP + second * kQSlice + row * 128;
   int32_t* status = a.shape.status;
   int it = 0, nmeet = 0;
-  auto meet = [&]() -> bool {  // the four warps of these heads; shared writes become visible
+  auto meet = [&]() -> bool {  // the eight warps; shared writes become visible
     __syncwarp();
-    if (lane == 0) mbar_arrive(&mi.meet[t]);
-    return tc::wait_warp(&mi.meet[t], nmeet++ & 1, &mi.quit, status);
+    if (lane == 0) mbar_arrive(&mi.meet);
+    return tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status);
   };
-  for (int n = 0;; ++n) {
-    const int slot = n % kSegs;
-    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, status)) return;
-    const ChunkSeg g = mi.seg[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&mi.seg_empty[slot]);
-    if (!g.valid) return;
+  ChunkSeg g;
+  for (int n = 0; next_piece(mi, n, status, g); ++n) {
     const int nt = g.i1 - g.i0, s = g.s0;
     const Pages pages(a, g);
-    float l[32], m = -INFINITY;  // sums of this thread's keys; maximum of head 32 t + lane
-#pragma unroll
-    for (int c = 0; c < 32; ++c) l[c] = 0.f;
-    bool none = true;  // no key seen yet in this piece
+    float l = 0.f, m = -INFINITY;
     for (int i = 0; i < nt; ++i, ++it) {
       // all that the scores are not needed for comes before they are waited for
-      const int key = tile_of(g, g.i0 + i) * kKeyTile + r;
-      const bool stored = key < g.L && pages.wanted(key >> a.page_shift);
-      const bool seen = key <= s && (a.shape.window == 0 || key > s - a.shape.window ||
-                                     key < a.shape.sink);
+      const int key0 = tile_of(g, g.i0 + i) * kKeyTile;
+      const int hi = s - key0 - key_in;
+      const int lo = a.shape.window > 0 ? hi - a.shape.window : -1;
+      const int sk = a.shape.sink - key0 - key_in;
+      uint32_t see = 0xFFFFFFFFu;
+      if (hi < 31 || (lo >= 0 && sk <= min(lo, 31))) {
+        auto below = [](int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1; };
+        see = below(hi + 1) & (~below(lo + 1) | below(sk));
+      }
+      const bool stored = key0 + l128 < g.L && pages.wanted((key0 + l128) >> a.page_shift);
       const bool ragged = !__all_sync(0xffffffffu, stored);
-      if (!tc::wait_warp(&mi.s_full, it & 1, &mi.quit, status)) return;
+      if (!tc::wait_warp(&mi.s_full[it & 1], (it >> 1) & 1, &mi.quit, status)) return;
       tc::fence_after();
       if (ragged) {
-        // rows without a loaded token would meet a probability of zero; 0 * NaN is not 0
+        // keys without a loaded row meet a probability of zero; 0 * NaN is not 0.  (The values
+        // before these have been multiplied: that was awaited for the last tile's P.)
+        if (it > 0 && !tc::wait_warp(&mi.o_done, (it - 1) & 1, &mi.quit, status)) return;
+        if (!tc::wait_warp(&mi.v_full, it & 1, &mi.quit, status)) return;
         if (!stored) {
-          const uint32_t base = smem + kKeys + 4 * t * kSlice + r * 128;
+          const uint32_t base = smem + kValues + 2 * t * kVSlice + l128 * 128;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < 16; ++e)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             base + (e >> 3) * kSlice + (e & 7) * 16),
+                             base + (e >> 3) * kVSlice + (e & 7) * 16),
                          "r"(0)
                          : "memory");
         }
         __syncwarp();
       }
-      // P with the maximum in use, in place of the scores, while the vote on it goes round
-      float p[32];
-      auto probabilities = [&](bool vote) {
-        uint32_t x[32];
-        tc::tmem_ld32(tmem + lanes + 32 * t, x);
-        float top = -INFINITY;
+      uint32_t x[32];
+      tc::tmem_ld32(tmem + lanes + (it & 1) * 64 + 32 * t, x);
+      if (see != 0xFFFFFFFFu) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 off = *reinterpret_cast<const float4*>(&mi.off[t][c]);
-          p[c] = fmaf(__uint_as_float(x[c]), a.scale_log2, off.x);
-          p[c + 1] = fmaf(__uint_as_float(x[c + 1]), a.scale_log2, off.y);
-          p[c + 2] = fmaf(__uint_as_float(x[c + 2]), a.scale_log2, off.z);
-          p[c + 3] = fmaf(__uint_as_float(x[c + 3]), a.scale_log2, off.w);
-        }
-        if (vote) {
+        for (int c = 0; c < 32; ++c)
+          if (!((see >> c) & 1)) x[c] = 0xFF800000u;  // -inf
+      }
+      __syncwarp();
+      float mxs[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(p[c], p[c + 1]));
-          const bool over = __any_sync(0xffffffffu, seen && (none || top > 8.f));
-          // round it: raise flag it % 3; flag (it + 1) % 3 was last read before the last vote
-          if (lane == 0) {
-            if (wq == 0) *(volatile int*)&mi.vote[t][(it + 1) % 3] = 0;
-            if (over) *(volatile int*)&mi.vote[t][it % 3] = 1;
-            mbar_arrive(&mi.meet[t]);
-          }
-        }
-        const uint32_t prow = smem + kP + r * 128;
+      for (int c = 0; c < 32; c += 4)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[4];
+        for (int e = 0; e < 2; ++e)
+          mxs[e] = tc::max3(mxs[e], __uint_as_float(x[c + 2 * e]),
+                            __uint_as_float(x[c + 2 * e + 1]));
+      const float mx = fmaxf(mxs[0], mxs[1]) * a.scale_log2;
+      // the vote goes round while the exponentials are computed: flag it % 3 is raised; flag
+      // (it + 1) % 3 was last read before the last vote
+      const bool over = __any_sync(0xffffffffu, mx > -INFINITY && !(mx - m <= 8.f));
+      if (lane == 0) {
+        if (threadIdx.x == 0) *(volatile int*)&mi.vote[(it + 1) % 3] = 0;
+        if (over) *(volatile int*)&mi.vote[it % 3] = 1;
+        mbar_arrive(&mi.meet);
+      }
+      float p[32], add;
+      uint32_t w[16];
+      auto probabilities = [&]() {
+        const float off = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int c = 8 * u + 2 * e;
-            p[c] = seen ? fast_exp2(p[c]) : 0.f;
-            p[c + 1] = seen ? fast_exp2(p[c + 1]) : 0.f;
-            w[e] = pack_bf16(p[c], p[c + 1]);
-          }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           prow + (((4 * t + u) ^ (r & 7)) << 4)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-        }
+        for (int c = 0; c < 32; ++c)
+          p[c] = fast_exp2(fmaf(__uint_as_float(x[c]), a.scale_log2, off));
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) sum[c & 3] += p[c];
+        add = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       };
-      probabilities(true);
-      tc::fence_async_smem();
-      if (!tc::wait_warp(&mi.meet[t], nmeet++ & 1, &mi.quit, status)) return;
-      if (*(volatile int*)&mi.vote[t][it % 3]) {
-        // raise the maximum: columns' maxima over the tile's keys, O^T and the sums rescaled
-        {
-          uint32_t x[32];
-          tc::tmem_ld32(tmem + lanes + 32 * t, x);
-          float v[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            v[c] = seen ? __uint_as_float(x[c]) * a.scale_log2 : -INFINITY;
-          mi.red[t][wq][lane] = across<true>(v);
-        }
+      probabilities();
+      if (!tc::wait_warp(&mi.meet, nmeet++ & 1, &mi.quit, status)) return;
+      // P's place and O are free once the last product with V is done
+      if (it > 0 && !tc::wait_warp(&mi.o_done, (it - 1) & 1, &mi.quit, status)) return;
+      if (*(volatile int*)&mi.vote[it % 3]) {
+        // raise the maximum of every row to what its four threads have seen
+        mi.red[t * 2 + second][row] = mx;
         if (!meet()) return;
-        const float up = fmaxf(fmaxf(fmaxf(mi.red[t][0][lane], mi.red[t][1][lane]),
-                                     fmaxf(mi.red[t][2][lane], mi.red[t][3][lane])),
+        const float up = fmaxf(fmaxf(fmaxf(mi.red[0][row], mi.red[1][row]),
+                                     fmaxf(mi.red[2][row], mi.red[3][row])),
                                m);
-        if (wq == 0) {
-          mi.fac[t][lane] = m == -INFINITY ? 0.f : fast_exp2(m - up);
-          mi.off[t][lane] = up == -INFINITY ? 0.f : -up;
-        }
+        const float f = up == -INFINITY ? 1.f : fast_exp2(m - up);
         m = up;
-        if (!meet()) return;
-        if (!none) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) l[c] *= mi.fac[t][c];
+        l *= f;
+        if (i > 0) {
+          tc::fence_after();
 #pragma unroll 1
-          for (int cb = 0; cb < 4; ++cb) {
+          for (int c0 = 0; c0 < 128; c0 += 32) {
             uint32_t o[32];
-            const uint32_t col = tmem + lanes + kO + cb * 64 + 32 * t;
+            const uint32_t col = tmem + lanes + kO + t * 128 + c0;
             tc::tmem_ld32(col, o);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              o[c] = __float_as_uint(__uint_as_float(o[c]) * mi.fac[t][c]);
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
             tc::tmem_st32(col, o);
           }
           tc::tmem_wait_st();
         }
-        none = false;
-        probabilities(false);
-        tc::fence_async_smem();
+        probabilities();
+        if (!meet()) return;  // red may be written again
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         p_row + (((4 * t + u) ^ (row & 7)) << 4)),
+                     "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
+                     : "memory");
+      tc::fence_async_smem();
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&mi.p_full);
-#pragma unroll
-      for (int c = 0; c < 32; ++c) l[c] += p[c];
+      if (lane == 0) tc::arrive_at_first(&mi.p_full);
+      l += add;
     }
     // ---- results
-    const float part = across<false>(l);
-    mi.red[t][wq][lane] = part;
+    mi.red[t * 2 + second][row] = l;
     if (!meet()) return;
-    const float sum = (mi.red[t][0][lane] + mi.red[t][1][lane]) +
-                      (mi.red[t][2][lane] + mi.red[t][3][lane]);
-    const int head = g.h * kHalf + 32 * t + lane;
-    if (wq == 0) {
-      mi.fac[t][lane] = g.part >= 0 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
-      if (g.part >= 0)
-        a.part_ml[(size_t)g.part * kHalf + 32 * t + lane] = make_float2(m, sum);
-      else
-        a.lse[(size_t)g.row0 * kHeads + head] =
-            sum > 0.f ? (m + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
-    }
-    if (!meet()) return;
-    if (!tc::wait_warp(&mi.o_full, n & 1, &mi.quit, status)) return;
+    l = (mi.red[0][row] + mi.red[1][row]) + (mi.red[2][row] + mi.red[3][row]);
+    if (!tc::wait_warp(&mi.o_done, (it - 1) & 1, &mi.quit, status)) return;
     tc::fence_after();
+    const int64_t orow = (int64_t)g.row0 * kHeads + rank * kHalf + row;
+    const int ch0 = t * 256 + second * 128;  // channels of this thread's columns
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
-    for (int cb = 0; cb < 4; ++cb) {
+    for (int c0 = 0; c0 < 128; c0 += 32) {
       uint32_t o[32];
-      tc::tmem_ld32(tmem + lanes + kO + cb * 64 + 32 * t, o);
-      const int ch = cb * 128 + r;
+      tc::tmem_ld32(tmem + lanes + kO + t * 128 + c0, o);
       if (g.part >= 0) {
-        float4* dst = reinterpret_cast<float4*>(
-            a.part_o + ((size_t)g.part * kDv + ch) * kHalf + 32 * t);
+        float4* dst = reinterpret_cast<float4*>(a.part_o) +
+                      ((size_t)g.part * (kDv / 4) + ((ch0 + c0) >> 2)) * kHalf + row;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+          dst[c * kHalf] =
+              make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                          __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
       } else {
-        uint16_t* dst =
-            a.out + ((size_t)g.row0 * kHeads + g.h * kHalf + 32 * t) * kDv + ch;
+        // four lanes turn their rows' 64 bytes, so that a store covers 64 bytes of a row
+        uint32_t v[4][4];  // [16-byte unit][word]
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          dst[(size_t)c * kDv] =
-              (uint16_t)pack_bf16(__uint_as_float(o[c]) * mi.fac[t][c], 0.f);
+        for (int c = 0; c < 16; ++c)
+          v[c >> 2][c & 3] = pack_bf16(__uint_as_float(o[2 * c]) * inv,
+                                       __uint_as_float(o[2 * c + 1]) * inv);
+#pragma unroll
+        for (int o2 = 1; o2 < 4; o2 <<= 1)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (!(u & o2)) {
+              const bool odd = lane & o2;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t got =
+                    __shfl_xor_sync(0xffffffffu, odd ? v[u][e] : v[u | o2][e], o2);
+                if (odd)
+                  v[u][e] = got;
+                else
+                  v[u | o2][e] = got;
+              }
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // row k of the four
+          *reinterpret_cast<uint4*>(a.out + (orow - (lane & 3) + k) * kDv + ch0 + c0 +
+                                    (lane & 3) * 8) =
+              make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
       }
+      __syncwarp();
     }
-    // the next piece's first raise of the maximum writes fac and off behind two meetings, and
-    // its products into O^T wait for this thread's arrival on p_full
+    if (t == 0 && second == 0) {
+      if (g.part >= 0)
+        a.part_ml[(size_t)g.part * kHalf + row] = make_float2(m, l);
+      else
+        a.lse[orow] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
     tc::fence_before();
+    if (!meet()) return;  // red may be written again
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_u32(smem_raw);
   Misc& mi = *reinterpret_cast<Misc*>(smem_raw + kMisc);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = tc::cluster_rank();
+  if (tid == 352) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+  }
   if (tid == 0) {
-    for (int i = 0; i < kGroups; ++i) {
-      mbar_init(&mi.full[i], 1);
-      mbar_init(&mi.empty[i], 1);
-    }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&mi.seg_full[i], 1);
-      mbar_init(&mi.seg_empty[i], 9);  // the issuing thread and eight softmax warps
+      // softmax, values', and the products' warp or the two that pass on
+      mbar_init(&mi.seg_empty[i], 10 + rank);
     }
     mbar_init(&mi.q_full, 1);
+    mbar_init(&mi.k_full, 1);
+    mbar_init(&mi.v_full, 1);
+    mbar_init(&mi.q_peer, 1);
+    mbar_init(&mi.k_peer, 1);
+    mbar_init(&mi.v_peer, 1);
     mbar_init(&mi.q_empty, 1);
-    mbar_init(&mi.s_full, 1);
-    mbar_init(&mi.p_full, 8);
-    mbar_init(&mi.o_full, 1);
+    mbar_init(&mi.k_empty, 1);
+    mbar_init(&mi.s_full[0], 1);
+    mbar_init(&mi.s_full[1], 1);
+    mbar_init(&mi.p_full, 16);  // the softmax warps of both CTAs
+    mbar_init(&mi.o_done, 1);
     mbar_init(&mi.drain, 1);
-    mbar_init(&mi.meet[0], 4);
-    mbar_init(&mi.meet[1], 4);
+    mbar_init(&mi.meet, 8);
     mi.quit = 0;
-    for (int i = 0; i < 6; ++i) (&mi.vote[0][0])[i] = 0;
-    for (int i = 0; i < 64; ++i) (&mi.off[0][0])[i] = 0.f;
+    for (int i = 0; i < 3; ++i) mi.vote[i] = 0;
     fence_mbar_init();
     // everything below reads what earlier kernels of the stream wrote
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  if (warp == 8) tc::tmem_alloc_all(&mi.tmem);
+  if (warp == 8) tc::pair_tmem_alloc_all(&mi.tmem);
   tc::fence_before();
   __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers are there
   tc::fence_after();
   const uint32_t tmem = mi.tmem;
   if (warp < 8) {
-    soften(a, smem, mi, tmem, warp >> 2);
+    soften(a, smem, mi, tmem, warp >> 2, rank);
   } else if (warp == 8) {
-    multiply(a, smem, mi, tmem);
-    __syncwarp();
-    if (tc::elect()) {
-      tc::commit(&mi.drain);
+    if (rank == 0) {
+      multiply(a, smem, mi, tmem);
+      __syncwarp();
+      if (tc::elect()) tc::pair_commit_here(&mi.drain);
+      __syncwarp();
       mbar_wait(&mi.drain, 0);
+    } else {
+      forward<true>(a, mi);
     }
-    __syncwarp();
-  } else {
-    produce(a, smem, mi, &qmap, &kmap);
-    __syncwarp();
+  } else if (warp == 9) {
+    produce_k(a, smem, mi, &qmap, &kmap, rank);
+  } else if (warp == 10) {
+    produce_v(a, smem, mi, &kmap, rank);
+  } else if (rank == 1) {
+    forward<false>(a, mi);
   }
+  __syncwarp();
   tc::fence_before();
   __syncthreads();
-  if (warp == 8) tc::tmem_free_all(tmem);
+  tc::cluster_sync();  // neither CTA reads the other's memory or arrives there any more
+  if (warp == 8) tc::pair_tmem_free_all(tmem);
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
-// Joins the pieces of the cut items, in piece order.  CTA = (cut item, 32 channels): a thread
-// sums 4 heads of 2 channels, the result is turned in shared memory and written by heads.
-// Also returns the item counter to zero for the next call.
-__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ part_o,
+// Joins the pieces of the cut items, in piece order.  CTA = (cut item, 16 channels): a thread
+// sums 4 channels of one head.  Also returns the item counter to zero for the next call.
+__global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ part_o,
                                                    const float2* __restrict__ part_ml,
                                                    const ChunkCut* __restrict__ cut,
-                                                   int32_t* ticket, uint16_t* __restrict__ out,
+                                                   uint16_t* __restrict__ out,
                                                    float* __restrict__ lse) {
-  __shared__ float tile[kHalf][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
-  const int c = blockIdx.x, ch0 = blockIdx.y * 32, tid = threadIdx.x;
-  if (c == 0 && blockIdx.y == 0 && tid == 0) *ticket = 0;
+  const int c = blockIdx.x, tid = threadIdx.x;
   const ChunkCut k = cut[c];
   if (k.nparts <= 0) return;
-  const int hq = (tid & 15) * 4, row = tid >> 4;  // heads hq.., channels row and row + 16
+  // heads side by side for the pieces (512 bytes a warp), four threads' channels a store
+  const int head = tid & 63, c4 = blockIdx.y * 4 + (tid >> 6);
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * c + 1 : 2 * (c + 2 * p)); };
-  float M[4], l[4], acc[2][4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    M[e] = -INFINITY;
-    l[e] = acc[0][e] = acc[1][e] = 0.f;
-  }
+  float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < k.nparts; ++p) M = fmaxf(M, part_ml[slot(p) * kHalf + head].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = 0; p < k.nparts; ++p) {
-    const float2* ml = part_ml + slot(p) * kHalf + hq;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) M[e] = fmaxf(M[e], ml[e].x);
+    const float2 ml = part_ml[slot(p) * kHalf + head];
+    const float4 v = part_o[(slot(p) * (kDv / 4) + c4) * kHalf + head];
+    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    l += f * ml.y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
   }
-#pragma unroll 4
-  for (int p = 0; p < k.nparts; ++p) {
-    const float2* ml = part_ml + slot(p) * kHalf + hq;
-    const float* src = part_o + (slot(p) * kDv + ch0 + row) * kHalf + hq;
-    const float4 v0 = *reinterpret_cast<const float4*>(src);
-    const float4 v1 = *reinterpret_cast<const float4*>(src + 16 * kHalf);
-    const float a0[4] = {v0.x, v0.y, v0.z, v0.w}, a1[4] = {v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float f = ml[e].x == -INFINITY ? 0.f : fast_exp2(ml[e].x - M[e]);
-      l[e] += f * ml[e].y;
-      acc[0][e] += f * a0[e];
-      acc[1][e] += f * a1[e];
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
-    tile[hq + e][row] = acc[0][e] * inv;
-    tile[hq + e][row + 16] = acc[1][e] * inv;
-    if (blockIdx.y == 0 && row == 0)
-      lse[(size_t)k.row0 * kHeads + k.h * kHalf + hq + e] =
-          l[e] > 0.f ? (M[e] + __log2f(l[e])) * 0.69314718055994531f : -INFINITY;
-  }
-  __syncthreads();
-  const int head = tid >> 2, c8 = (tid & 3) * 8;
-  const float* src = &tile[head][c8];
-  *reinterpret_cast<uint4*>(out + ((size_t)k.row0 * kHeads + k.h * kHalf + head) * kDv + ch0 +
-                            c8) = make_uint4(pack_bf16(src[0], src[1]), pack_bf16(src[2], src[3]),
-                                             pack_bf16(src[4], src[5]),
-                                             pack_bf16(src[6], src[7]));
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int64_t row = (int64_t)k.row0 * kHeads + k.h * kHalf + head;
+  reinterpret_cast<uint2*>(out + row * kDv)[c4] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (c4 == 0)
+    lse[row] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace chunk_mla
@@ -567,7 +604,7 @@ cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t 
   a.shape.window = c.window < longest ? c.window : longest;
   a.shape.cap = (int64_t)g.max_pages * g.P;
   a.shape.status = c.status;
-  a.shape.ticket = c.ticket;
+  a.shape.ticket = nullptr;
   a.page_table = c.page_table;
   a.kv = static_cast<const uint8_t*>(c.k_cache);
   a.out = static_cast<uint16_t*>(c.out);
@@ -591,10 +628,10 @@ cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   void* args[] = {&qm, &km, &a};
-  if ((e = chunk_launch(fn, dim3(c.n_sm), kThreads, kSmem, stream, args)) != cudaSuccess)
+  if ((e = chunk_launch(fn, dim3(c.n_sm & ~1), kThreads, kSmem, stream, args)) != cudaSuccess)
     return e;
-  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.shape.ticket, &a.out, &a.lse};
-  return chunk_launch(reinterpret_cast<const void*>(join_kernel), dim3(c.n_sm, kDv / 32), 256, 0,
+  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.out, &a.lse};
+  return chunk_launch(reinterpret_cast<const void*>(join_kernel), dim3(c.n_sm & ~1, kDv / 16), 256, 0,
                       stream, jargs);
 }
 

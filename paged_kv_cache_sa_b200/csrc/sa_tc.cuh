@@ -107,10 +107,91 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* quit,
     }
   }
 }
+// The same where the other CTA of the cluster arrives too.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, int* quit,
+                                             int32_t* status) {
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+      if (ok) return true;
+    }
+    if (*(volatile int*)quit) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *(volatile int*)quit = 1;
+      report(status, SA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
 // The same for a whole warp: one answer for all lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* quit,
                                           int32_t* status) {
   return __all_sync(0xffffffffu, wait(bar, parity, quit, status));
+}
+
+// ---- the same for a pair of CTAs (a cluster of two) that works on one tile: M = 128 rows, 64 of
+// A in each CTA's shared memory, half of B's N rows in each.  D: lanes 0-63 of a CTA hold its 64
+// rows' first N / 2 columns, lanes 64-127 the same rows' other N / 2.  The even CTA issues.
+__device__ __forceinline__ void pair_tmem_alloc_all(uint32_t* slot) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(slot)),
+               "r"(512)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_free_all(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(512)
+               : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate)
+      : "memory");
+}
+// arrives on the barrier at this place in both CTAs
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// arrives here only
+__device__ __forceinline__ void pair_commit_here(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// arrive on the barrier at this place in CTA 0 of the cluster
+__device__ __forceinline__ void arrive_at_first(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\t"
+      "mapa.shared::cluster.u32 r, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // ---- arithmetic on pairs of fp32 (one instruction for both) ------------------------------
@@ -147,6 +228,11 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ bool wait_cluster_warp(uint64_t* bar, uint32_t parity, int* quit,
+                                                  int32_t* status) {
+  return __all_sync(0xffffffffu, wait_cluster(bar, parity, quit, status));
 }
 
 // tiled TMA loads global -> shared (no multicast); x * 2 bytes is a multiple of 16
