@@ -8,16 +8,18 @@
 //   O += P V      (128 x 512 x 128)  takes 256,
 // and two score tiles fit beside the accumulator; one CTA alone would need all 512 columns for
 // O.  (Alone, with 64 heads a CTA and both products transposed, every product has N = 64 and
-// takes as long as one with N = 128: 1.60 ms instead of TIME for 256 + 100 rows at 16K / 5K.)
+// takes as long as one with N = 128: 1.60 ms instead of 1.09 for 256 + 100 rows at 16K / 5K.)
 // Of a key tile a CTA loads what its half of the products reads: 64 keys of all 576 channels
 // as B of the first (72 KB), 256 channels of all 128 keys as B of the second (64 KB), with
 // 72 KB of queries and 16 KB of probabilities.  The next tile's keys come in while this one's
-// softmax and second product run, the next values during the next scores.
+// softmax and second product run, the next values during the next scores, both in parts that
+// follow the products through the one buffer.  Copies of both CTAs are counted at the even one,
+// which issues the products.
 // A thread has one row and 32 of its 128 scores, so a row's maximum crosses four threads.  It
 // is only taken when some score exceeds the maximum in use by more than 2^8 (which a vote
 // finds); sums stay in the threads until the end.
 // Warps 0-3 and 4-7: softmax; 8: issues the products (even CTA); 9: work list, queries and
-// keys; 10: values; 8 and 11 of the odd CTA: tell the even one what has been loaded.
+// keys; 10: values.
 #include "sa_chunk.cuh"
 #include "sa_internal.h"
 #include "sa_tc.cuh"
@@ -30,6 +32,9 @@ constexpr int kD = 576, kDv = 512, kHeads = 128;
 constexpr int kHalf = 64;  // heads of a CTA, and keys that it loads for the scores
 constexpr int kThreads = 384;
 constexpr int kSegs = 2;
+// parts of a key tile that are loaded and given back by themselves: three slices of 64 channels
+// for the scores, one block of 256 channels of the values
+constexpr int kKGroups = 3, kVGroups = 2;
 constexpr uint32_t kQSlice = kHalf * 128;     // 64 rows of 64 channels
 constexpr uint32_t kVSlice = kKeyTile * 128;  // 128 keys' 64 channels
 constexpr uint32_t kKeys = 9 * kQSlice;       // queries first
@@ -42,9 +47,9 @@ struct Misc {
   float red[4][64];  // of a row's four threads
   ChunkSeg seg[kSegs];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t q_full, k_full, v_full;     // this CTA's loads
-  uint64_t q_peer, k_peer, v_peer;     // the other's (at the even CTA)
-  uint64_t q_empty, k_empty, s_full[2], p_full, o_done, drain, meet;
+  uint64_t q_full, k_full[kKGroups], v_full[kVGroups];  // at the even CTA, for both
+  uint64_t q_empty, k_empty[kKGroups], v_empty[kVGroups], v_here;
+  uint64_t s_full[2], p_full, o_done, drain, meet;
   uint32_t tmem;
   int quit;
   int vote[3];
@@ -81,32 +86,37 @@ struct Pages {
   }
 };
 
-// Copies of one piece's tiles.  V: 256 channels of all keys (a lane: slice lane % 4, pages
-// lane / 4, + 8, ...), else 64 keys of all channels (a lane: slices lane % 9 of page lane / 9,
-// in as many rounds as it takes).  `it`: tiles before the piece; `free`: completes once per tile.
+// Copies of one piece's tiles, counted at the even CTA.  V: this CTA's 128 channels of each block
+// of all keys, else its 64 keys of all channels; a lane copies one slice of one page.  `it`: tiles
+// before the piece.
 template <bool V>
 __device__ __forceinline__ bool load_tiles(const Args& a, uint32_t smem, Misc& mi,
                                            const ChunkSeg& g, const CUtensorMap* map, int it,
-                                           uint32_t rank) {
+                                           int rank) {
+  constexpr int kGroups = V ? kVGroups : kKGroups, kSlices = V ? 2 : 3;
   const int lane = threadIdx.x & 31, shift = a.page_shift;
-  const int ppt = kKeyTile >> shift, mine = V ? ppt : ppt >> 1;  // pages of a tile; of this copy
+  const int ppt = kKeyTile >> shift;                // pages of a tile (2, 4 or 8),
+  const int mine = V ? ppt : ppt >> 1;              // of this CTA's copies
+  const int from = V ? 0 : rank * mine;             // and the first of those
   const int nt = g.i1 - g.i0, last_page = (g.L - 1) >> shift;
   const Pages pages(a, g);
   const int32_t* row = a.page_table + (size_t)g.b * a.max_pages;
   const uint64_t policy = tc::l2_normal();
-  uint64_t* full = V ? &mi.v_full : &mi.k_full;
-  uint64_t* empty = V ? &mi.o_done : &mi.k_empty;
-  // lane p < mine looks up page p of the copy, two tiles ahead; entries are checked when used
+  uint64_t* full = V ? mi.v_full : mi.k_full;
+  uint64_t* empty = V ? mi.v_empty : mi.k_empty;
+  const uint32_t full_at = tc::at_first(full);
+  const int pg = lane / kSlices, sl = lane % kSlices;
+  // lane p < ppt looks up page p of a tile, two tiles ahead; entries are checked when used
   auto wanted = [&](int i, int& lp) {
-    lp = tile_of(g, g.i0 + i) * ppt + (V ? 0 : (int)rank * mine) + lane;
-    return lane < mine && lp <= last_page && pages.wanted(lp);
+    lp = tile_of(g, g.i0 + i) * ppt + lane;
+    return lane < ppt && lp <= last_page && pages.wanted(lp);
   };
   int p0 = -1, p1 = -1, lp;
   for (int i = -2; i < nt; ++i) {
     int p2 = -1;
     if (i + 2 < nt && wanted(i + 2, lp)) {
       p2 = row[lp];
-      if (!V && p2 >= 0 && p2 < a.n_pool)  // ask the page into L2
+      if (!V && p2 >= 0 && p2 < a.n_pool && lane / mine == rank)  // ask the page into L2
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                          a.kv + (size_t)p2 * a.P * (kD * 2)),
                      "r"(a.P * (kD * 2))
@@ -119,22 +129,22 @@ __device__ __forceinline__ bool load_tiles(const Args& a, uint32_t smem, Misc& m
         copy = false;
       }
       const unsigned have = __ballot_sync(0xffffffffu, copy);
-      if (it + i > 0 &&
-          !tc::wait_warp(empty, (it + i - 1) & 1, &mi.quit, a.shape.status))
-        return false;
-      constexpr int kSlices = V ? 4 : 9;
-      if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * kSlices * a.P * 128);
-      __syncwarp();
-      for (int e0 = 0; e0 < mine * kSlices; e0 += 32) {
-        const int e = e0 + lane, pg = min(e / kSlices, mine - 1), sl = e % kSlices;
-        const int ph = __shfl_sync(0xffffffffu, p0, pg);
-        if (e < mine * kSlices && ((have >> pg) & 1)) {
-          // V: slices 0, 1 are channels 128 rank .. of the first 256, 2, 3 of the others
-          const int ch = V ? (sl >> 1) * 256 + (int)rank * 128 + (sl & 1) * 64 : sl * 64;
-          tc::tma_2d(smem + (V ? kValues + sl * kVSlice : kKeys + sl * kQSlice) +
-                         ((uint32_t)pg << shift) * 128,
-                     map, ch, ph << shift, full, policy);
-        }
+      const int ph = __shfl_sync(0xffffffffu, p0, from + (pg < mine ? pg : 0));
+      const bool go = pg < mine && ((have >> (from + pg)) & 1);
+      // bytes of both CTAs: each half's pages once (V: every page twice)
+      const uint32_t bytes = __popc(have) * (V ? 2 : 1) * kSlices * a.P * 128;
+      for (int gr = 0; gr < kGroups; ++gr) {
+        if (it + i > 0 &&
+            !tc::wait_warp(&empty[gr], (it + i - 1) & 1, &mi.quit, a.shape.status))
+          return false;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[gr], bytes);
+        __syncwarp();
+        const int slice = gr * kSlices + sl;
+        if (go)
+          tc::pair_tma_2d(smem + (V ? kValues + slice * kVSlice : kKeys + slice * kQSlice) +
+                              ((uint32_t)pg << shift) * 128,
+                          map, V ? gr * 256 + rank * 128 + sl * 64 : slice * 64, ph << shift,
+                          full_at + gr * 8, policy);
       }
     }
     p0 = p1;
@@ -145,7 +155,7 @@ __device__ __forceinline__ bool load_tiles(const Args& a, uint32_t smem, Misc& m
 
 __device__ __forceinline__ void produce_k(const Args& a, uint32_t smem, Misc& mi,
                                           const CUtensorMap* qmap, const CUtensorMap* kmap,
-                                          uint32_t rank) {
+                                          int rank) {
   const int lane = threadIdx.x & 31;
   int32_t* status = a.shape.status;
   ChunkSched sched;
@@ -168,18 +178,20 @@ __device__ __forceinline__ void produce_k(const Args& a, uint32_t smem, Misc& mi
     }
     if (!more) return;
     if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, status)) break;
-    if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, 9 * kQSlice);
+    if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&mi.q_full, 2 * 9 * kQSlice);
     __syncwarp();
     if (lane < 9)
-      tc::tma_3d(smem + lane * kQSlice, qmap, lane * 64, g.h * kHalf, g.row0, &mi.q_full);
+      tc::pair_tma_3d(smem + lane * kQSlice, qmap, lane * 64, g.h * kHalf, g.row0,
+                      tc::at_first(&mi.q_full));
     if (!load_tiles<false>(a, smem, mi, g, kmap, it, rank)) break;
     it += g.i1 - g.i0;
   }
   // given up: copies in flight land (bounded) before shared memory goes away
-  for (int ph = 0; ph < 2; ++ph) {
-    mbar_wait(&mi.k_full, ph);
-    mbar_wait(&mi.q_full, ph);
-  }
+  if (rank == 0)
+    for (int ph = 0; ph < 2; ++ph) {
+      for (int gr = 0; gr < kKGroups; ++gr) mbar_wait(&mi.k_full[gr], ph);
+      mbar_wait(&mi.q_full, ph);
+    }
 }
 
 // Reads the list as the other warps do: the next piece, or false.
@@ -193,30 +205,13 @@ __device__ __forceinline__ bool next_piece(Misc& mi, int n, int32_t* status, Chu
 }
 
 __device__ __forceinline__ void produce_v(const Args& a, uint32_t smem, Misc& mi,
-                                          const CUtensorMap* kmap, uint32_t rank) {
+                                          const CUtensorMap* kmap, int rank) {
   ChunkSeg g;
   for (int n = 0; next_piece(mi, n, a.shape.status, g); ++n)
     if (!load_tiles<true>(a, smem, mi, g, kmap, g.it0, rank)) break;
-  if (*(volatile int*)&mi.quit)
-    for (int ph = 0; ph < 2; ++ph) mbar_wait(&mi.v_full, ph);
-}
-
-// The odd CTA: passes on that its queries and keys (its values) have come.
-template <bool V>
-__device__ __forceinline__ void forward(const Args& a, Misc& mi) {
-  const bool one = (threadIdx.x & 31) == 0;
-  int32_t* status = a.shape.status;
-  ChunkSeg g;
-  for (int n = 0; next_piece(mi, n, status, g); ++n) {
-    if (!V) {
-      if (!tc::wait_warp(&mi.q_full, n & 1, &mi.quit, status)) return;
-      if (one) tc::arrive_at_first(&mi.q_peer);
-    }
-    for (int it = g.it0; it < g.it0 + g.i1 - g.i0; ++it) {
-      if (!tc::wait_warp(V ? &mi.v_full : &mi.k_full, it & 1, &mi.quit, status)) return;
-      if (one) tc::arrive_at_first(V ? &mi.v_peer : &mi.k_peer);
-    }
-  }
+  if (rank == 0 && *(volatile int*)&mi.quit)
+    for (int ph = 0; ph < 2; ++ph)
+      for (int gr = 0; gr < kVGroups; ++gr) mbar_wait(&mi.v_full[gr], ph);
 }
 
 // The even CTA: all products.
@@ -225,47 +220,55 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
   constexpr uint32_t id_o = tc::idesc(128, 256, false, true);
   int32_t* status = a.shape.status;
   int it = 0;
-  auto both = [&](uint64_t* own, uint64_t* peer, uint32_t parity) {
-    return tc::wait_warp(own, parity & 1, &mi.quit, status) &&
-           tc::wait_cluster_warp(peer, parity & 1, &mi.quit, status);
+  // (copies into the other CTA's shared memory are counted here too: cluster scope)
+  auto arrived = [&](uint64_t* bar, uint32_t parity) {
+    const bool r = tc::wait_cluster_warp(bar, parity & 1, &mi.quit, status);
+    tc::fence_after();
+    return r;
   };
   auto scores = [&](int x, bool last) -> bool {  // S of tile x
-    if (!both(&mi.k_full, &mi.k_peer, x)) return false;
-    tc::fence_after();
-    if (tc::elect()) {
 #pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * kQSlice + (kk & 3) * 32;
-        tc::pair_mma(tmem + (x & 1) * 64, tc::desc(smem + o), tc::desc(smem + kKeys + o), id_s,
-                     kk != 0);
+    for (int gr = 0; gr < kKGroups; ++gr) {
+      if (!arrived(&mi.k_full[gr], x)) return false;
+      if (tc::elect()) {
+#pragma unroll
+        for (int kk = 12 * gr; kk < 12 * gr + 12; ++kk) {
+          const uint32_t o = (kk >> 2) * kQSlice + (kk & 3) * 32;
+          tc::pair_mma(tmem + (x & 1) * 64, tc::desc(smem + o), tc::desc(smem + kKeys + o), id_s,
+                       kk != 0);
+        }
+        tc::pair_commit(&mi.k_empty[gr]);
+        if (gr == kKGroups - 1) {
+          tc::pair_commit(&mi.s_full[x & 1]);
+          if (last) tc::pair_commit(&mi.q_empty);
+        }
       }
-      tc::pair_commit(&mi.s_full[x & 1]);
-      tc::pair_commit(&mi.k_empty);
-      if (last) tc::pair_commit(&mi.q_empty);
+      __syncwarp();
     }
-    __syncwarp();
     return true;
   };
   for (int n = 0;; ++n) {
     ChunkSeg g;
     if (!next_piece(mi, n, status, g)) return;
     const int nt = __shfl_sync(0xffffffffu, g.i1 - g.i0, 0);
-    if (!both(&mi.q_full, &mi.q_peer, n) || !scores(it, nt == 1)) return;
+    if (!arrived(&mi.q_full, n) || !scores(it, nt == 1)) return;
     for (int i = 0; i < nt; ++i, ++it) {
       if (i + 1 < nt && !scores(it + 1, i + 2 == nt)) return;
-      if (!both(&mi.v_full, &mi.v_peer, it) ||
-          !tc::wait_cluster_warp(&mi.p_full, it & 1, &mi.quit, status))
-        return;
-      tc::fence_after();
+      if (!arrived(&mi.v_full[0], it) || !arrived(&mi.v_full[1], it)) return;
+      if (tc::elect()) tc::pair_commit(&mi.v_here);
+      __syncwarp();
+      if (!arrived(&mi.p_full, it)) return;
       if (tc::elect()) {
 #pragma unroll
-        for (int kk = 0; kk < kKeyTile / 16; ++kk)
+        for (int cb = 0; cb < 2; ++cb) {
 #pragma unroll
-          for (int cb = 0; cb < 2; ++cb)
+          for (int kk = 0; kk < kKeyTile / 16; ++kk)
             tc::pair_mma(tmem + kO + cb * 128,
                          tc::desc(smem + kP + (kk >> 2) * kQSlice + (kk & 3) * 32),
                          tc::desc(smem + kValues + 2 * cb * kVSlice + kk * 2048, kVSlice), id_o,
                          !(i == 0 && kk == 0));
+          tc::pair_commit(&mi.v_empty[cb]);
+        }
         tc::pair_commit(&mi.o_done);
       }
       __syncwarp();
@@ -275,7 +278,7 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
 
 // softmax and epilogue: columns [32 t, 32 t + 32) of a score tile's 64, accumulator block t
 __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, uint32_t tmem,
-                                       int t, uint32_t rank) {
+                                       int t, int rank) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 3;
   const int l128 = wq * 32 + lane;                   // lane of tensor memory
   const int row = l128 & 63, second = l128 >> 6;     // head of the CTA; half of the columns
@@ -313,7 +316,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         // keys without a loaded row meet a probability of zero; 0 * NaN is not 0.  (The values
         // before these have been multiplied: that was awaited for the last tile's P.)
         if (it > 0 && !tc::wait_warp(&mi.o_done, (it - 1) & 1, &mi.quit, status)) return;
-        if (!tc::wait_warp(&mi.v_full, it & 1, &mi.quit, status)) return;
+        if (!tc::wait_warp(&mi.v_here, it & 1, &mi.quit, status)) return;
         if (!stored) {
           const uint32_t base = smem + kValues + 2 * t * kVSlice + l128 * 128;
 #pragma unroll
@@ -475,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t smem = smem_u32(smem_raw);
   Misc& mi = *reinterpret_cast<Misc*>(smem_raw + kMisc);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t rank = tc::cluster_rank();
+  const int rank = (int)tc::cluster_rank();
   if (tid == 352) {
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
@@ -483,17 +486,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&mi.seg_full[i], 1);
-      // softmax, values', and the products' warp or the two that pass on
-      mbar_init(&mi.seg_empty[i], 10 + rank);
+      mbar_init(&mi.seg_empty[i], 10 - rank);  // softmax, values', even: products' warp
     }
     mbar_init(&mi.q_full, 1);
-    mbar_init(&mi.k_full, 1);
-    mbar_init(&mi.v_full, 1);
-    mbar_init(&mi.q_peer, 1);
-    mbar_init(&mi.k_peer, 1);
-    mbar_init(&mi.v_peer, 1);
     mbar_init(&mi.q_empty, 1);
-    mbar_init(&mi.k_empty, 1);
+    for (int i = 0; i < kKGroups; ++i) {
+      mbar_init(&mi.k_full[i], 1);
+      mbar_init(&mi.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVGroups; ++i) {
+      mbar_init(&mi.v_full[i], 1);
+      mbar_init(&mi.v_empty[i], 1);
+    }
+    mbar_init(&mi.v_here, 1);
     mbar_init(&mi.s_full[0], 1);
     mbar_init(&mi.s_full[1], 1);
     mbar_init(&mi.p_full, 16);  // the softmax warps of both CTAs
@@ -521,15 +526,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (tc::elect()) tc::pair_commit_here(&mi.drain);
       __syncwarp();
       mbar_wait(&mi.drain, 0);
-    } else {
-      forward<true>(a, mi);
     }
   } else if (warp == 9) {
     produce_k(a, smem, mi, &qmap, &kmap, rank);
   } else if (warp == 10) {
     produce_v(a, smem, mi, &kmap, rank);
-  } else if (rank == 1) {
-    forward<false>(a, mi);
   }
   __syncwarp();
   tc::fence_before();
