@@ -8,7 +8,7 @@
 //   O += P V      (128 x 512 x 128)  takes 256,
 // and two score tiles fit beside the accumulator; one CTA alone would need all 512 columns for
 // O.  (Alone, with 64 heads a CTA and both products transposed, every product has N = 64 and
-// takes as long as one with N = 128: 1.60 ms instead of 1.09 for 256 + 100 rows at 16K / 5K.)
+// takes as long as one with N = 128: 1.60 ms instead of 0.98 for 256 + 100 rows at 16K / 5K.)
 // Of a key tile a CTA loads what its half of the products reads: 64 keys of all 576 channels
 // as B of the first (72 KB), 256 channels of all 128 keys as B of the second (64 KB), with
 // 72 KB of queries and 16 KB of probabilities.  The next tile's keys come in while this one's
@@ -116,7 +116,7 @@ __device__ __forceinline__ bool load_tiles(const Args& a, uint32_t smem, Misc& m
     int p2 = -1;
     if (i + 2 < nt && wanted(i + 2, lp)) {
       p2 = row[lp];
-      if (!V && p2 >= 0 && p2 < a.n_pool && lane / mine == rank)  // ask the page into L2
+      if (!V && g.once && p2 >= 0 && p2 < a.n_pool && lane / mine == rank)  // ask it into L2
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                          a.kv + (size_t)p2 * a.P * (kD * 2)),
                      "r"(a.P * (kD * 2))
@@ -220,9 +220,8 @@ __device__ __forceinline__ void multiply(const Args& a, uint32_t smem, Misc& mi,
   constexpr uint32_t id_o = tc::idesc(128, 256, false, true);
   int32_t* status = a.shape.status;
   int it = 0;
-  // (copies into the other CTA's shared memory are counted here too: cluster scope)
   auto arrived = [&](uint64_t* bar, uint32_t parity) {
-    const bool r = tc::wait_cluster_warp(bar, parity & 1, &mi.quit, status);
+    const bool r = tc::wait_warp(bar, parity & 1, &mi.quit, status);
     tc::fence_after();
     return r;
   };
