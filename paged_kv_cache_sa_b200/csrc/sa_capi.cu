@@ -682,7 +682,7 @@ SA_EXPORT int sa_attend_chunk(const sa_geom* g, const void* q, int n_tokens,
   if (n_tokens < 0 || !q || !cu_new || !k_cache || !page_table || !seq_lens || !out || !lse)
     return SA_ERR_INVALID_ARG;
   if (!g->v_aliases_k && !v_cache) return SA_ERR_INVALID_ARG;
-  if (sink < 0 || window < 0 || !(scale > 0.f) || !(scale < 3.0e38f)) return SA_ERR_INVALID_ARG;
+  if (sink < 0 || window < 0 || !(scale > 0.f) || !(scale <= 2.0e38f)) return SA_ERR_INVALID_ARG;
   const void* vc = g->v_aliases_k ? k_cache : v_cache;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(vc) || !aligned16(out))
     return SA_ERR_INVALID_ARG;
