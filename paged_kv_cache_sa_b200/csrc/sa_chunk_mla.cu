@@ -8,7 +8,7 @@
 //   O += P V      (128 x 512 x 128)  takes 256,
 // and two score tiles fit beside the accumulator; one CTA alone would need all 512 columns for
 // O.  (Alone, with 64 heads a CTA and both products transposed, every product has N = 64 and
-// takes as long as one with N = 128: 1.60 ms instead of 0.98 for 256 + 100 rows at 16K / 5K.)
+// takes as long as one with N = 128: 1.60 ms instead of 0.90 for 256 + 100 rows at 16K / 5K.)
 // Of a key tile a CTA loads what its half of the products reads: 64 keys of all 576 channels
 // as B of the first (72 KB), 256 channels of all 128 keys as B of the second (64 KB), with
 // 72 KB of queries and 16 KB of probabilities.  The next tile's keys come in while this one's
