@@ -539,8 +539,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
 }
 
-// Joins the pieces of the cut items, in piece order.  CTA = (cut item, 16 channels): a thread
-// sums 4 channels of one head.  Also returns the item counter to zero for the next call.
+// Joins the pieces of the cut items, in piece order.  CTA = (cut item, 64 channels): a thread sums
+// 16 channels of one head.
 __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ part_o,
                                                    const float2* __restrict__ part_ml,
                                                    const ChunkCut* __restrict__ cut,
@@ -552,28 +552,39 @@ __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ pa
   const int c = blockIdx.x, tid = threadIdx.x;
   const ChunkCut k = cut[c];
   if (k.nparts <= 0) return;
-  // heads side by side for the pieces (512 bytes a warp), four threads' channels a store
-  const int head = tid & 63, c4 = blockIdx.y * 4 + (tid >> 6);
+  // heads side by side (512 bytes of a piece a warp)
+  const int head = tid & 63, c4 = blockIdx.y * 16 + (tid >> 6) * 4;
   auto slot = [&](int p) { return (size_t)(p == 0 ? 2 * c + 1 : 2 * (c + 2 * p)); };
   float M = -INFINITY, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int p = 0; p < k.nparts; ++p) M = fmaxf(M, part_ml[slot(p) * kHalf + head].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = 0; p < k.nparts; ++p) {
     const float2 ml = part_ml[slot(p) * kHalf + head];
-    const float4 v = part_o[(slot(p) * (kDv / 4) + c4) * kHalf + head];
+    const float4* src = part_o + (slot(p) * (kDv / 4) + c4) * kHalf + head;
     const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
     l += f * ml.y;
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float4 v = src[e * kHalf];
+      acc[e].x += f * v.x;
+      acc[e].y += f * v.y;
+      acc[e].z += f * v.z;
+      acc[e].w += f * v.w;
+    }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int64_t row = (int64_t)k.row0 * kHeads + k.h * kHalf + head;
-  reinterpret_cast<uint2*>(out + row * kDv)[c4] =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  uint4* dst = reinterpret_cast<uint4*>(out + row * kDv + c4 * 4);
+#pragma unroll
+  for (int e = 0; e < 4; e += 2)
+    dst[e >> 1] = make_uint4(pack_bf16(acc[e].x * inv, acc[e].y * inv),
+                             pack_bf16(acc[e].z * inv, acc[e].w * inv),
+                             pack_bf16(acc[e + 1].x * inv, acc[e + 1].y * inv),
+                             pack_bf16(acc[e + 1].z * inv, acc[e + 1].w * inv));
   if (c4 == 0)
     lse[row] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -631,7 +642,7 @@ cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t 
   if ((e = chunk_launch(fn, dim3(c.n_sm & ~1), kThreads, kSmem, stream, args)) != cudaSuccess)
     return e;
   void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.out, &a.lse};
-  return chunk_launch(reinterpret_cast<const void*>(join_kernel), dim3(c.n_sm & ~1, kDv / 16), 256, 0,
+  return chunk_launch(reinterpret_cast<const void*>(join_kernel), dim3(c.n_sm & ~1, kDv / 64), 256, 0,
                       stream, jargs);
 }
 
