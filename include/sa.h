@@ -329,8 +329,9 @@ int sa_prune_compact(const sa_geom* g, const void* k_cache, const void* v_cache,
  * A call takes a ragged batch of n_tokens rows: rows [cu_new[b], cu_new[b+1]) are the new
  * tokens of sequence b (n_b of them, possibly none), in order.  seq_lens[b] is the length
  * AFTER the append, as every other call of this library expects it, so new token i of
- * sequence b lives in slot s = seq_lens[b] - n_b + i.  Rows at or behind cu_new[B] belong to
- * no sequence: nothing is read for them and their outputs keep their contents.
+ * sequence b lives in slot s = seq_lens[b] - n_b + i.  Rows in front of cu_new[0] and from
+ * cu_new[B] on belong to no sequence: what they hold is not used and their outputs keep their
+ * contents.
  * n_tokens = 0 is legal and launches nothing.  A sequence with cu_new[b] < 0,
  * cu_new[b] > cu_new[b+1], cu_new[b+1] > n_tokens, seq_lens[b] < n_b or seq_lens[b] >
  * max_pages * P is left out and reported as SA_ERR_DEVICE_CHECK.
@@ -374,12 +375,15 @@ int sa_append_kv(const sa_geom* g, const void* q, int64_t q_stride, const void* 
  *   x_t = scale * q . k_t;  out = sum_t softmax(x)_t v_t;  lse = log sum_t exp(x_t).
  *   q [n_tokens][Hq][Dk] bf16, out [n_tokens][Hq][Dv] bf16 (the operand of the output
  *   projection; half the bytes of the decode calls' fp32), lse [n_tokens][Hq] fp32.
- * scale must be positive and finite.  Scores, softmax statistics and sums are fp32; the
+ * scale: positive, at most 2e38 (the softmax works in base 2).  Scores, softmax statistics and sums are fp32; the
  * probabilities are rounded to bf16 (relative to a running maximum) for the product with V,
- * and out once at the end.  Storage behind seq_lens[b] is never used.  Results do not depend
- * on what else runs and repeat bit for bit.  A page-table entry outside [0, n_pool) of a
- * page holding visible tokens is reported as SA_ERR_DEVICE_CHECK; the rows that see such a
- * page are then unspecified.  One new token per sequence (n_b = 1) is the dense decode.
+ * and out once at the end.  Storage behind seq_lens[b] is never used, and neither are pages
+ * all of whose tokens a window hides (their table entries may be anything).  The same call
+ * repeats bit for bit; a row's last bits depend on how the batch divides the work.  A
+ * page-table entry outside [0, n_pool) of a page holding visible tokens is reported as
+ * SA_ERR_DEVICE_CHECK; the rows of that sequence are then unspecified.  Whether a page that
+ * only holds later tokens of the sequence than a row may see is read for that row is not
+ * specified (its tokens are valid and finite by the precondition above).  One new token per sequence (n_b = 1) is the dense decode.
  * sa_chunk_workspace_size: bytes needed for up to n_tokens rows (0 on invalid arguments);
  * any decode workspace of at least that size serves too. */
 size_t sa_chunk_workspace_size(const sa_geom* g, int n_tokens);

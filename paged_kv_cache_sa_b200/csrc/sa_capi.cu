@@ -705,7 +705,6 @@ SA_EXPORT int sa_attend_chunk(const sa_geom* g, const void* q, int n_tokens,
   c.lse = lse;
   c.scratch = static_cast<uint8_t*>(ws) + 256;
   c.status = &static_cast<WsHeader*>(ws)->status_bits;
-  c.ticket = &static_cast<WsHeader*>(ws)->pad[1];
   c.n_sm = n_sm;
   return cuda_status(launch_chunk(*g, c, static_cast<cudaStream_t>(stream)));
 }

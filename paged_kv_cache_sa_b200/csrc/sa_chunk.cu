@@ -667,13 +667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of the cut items: out = sum_p 2^(m_p - M) O_p / L.  A CTA has eight rows of
 // one item; its eight warps take every eighth piece, a lane one row and every fourth 16-byte
-// group of its channels; the warps' sums meet in shared memory in warp order.  Also returns the
-// item counter to zero for the next call.
+// group of its channels; the warps' sums meet in shared memory in warp order.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ part_o,
                                                    const float2* __restrict__ part_ml,
                                                    const ChunkCut* __restrict__ cut,
-                                                   int32_t* ticket, uint16_t* __restrict__ out,
+                                                   uint16_t* __restrict__ out,
                                                    float* __restrict__ lse, int rows_cap, int Hq,
                                                    int G, int TB) {
   constexpr int C = D / 16;  // 16-byte groups of a lane
@@ -683,7 +682,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float4* __restrict__ pa
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
-  if (c == 0 && blockIdx.y == 0 && threadIdx.x == 0) *ticket = 0;
   const ChunkCut k = cut[c];
   if (k.nparts <= 0) return;
   const int r0 = blockIdx.y * 8;
@@ -778,7 +776,6 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   a.shape.window = c.window < longest ? c.window : longest;
   a.shape.cap = (int64_t)g.max_pages * g.P;
   a.shape.status = c.status;
-  a.shape.ticket = c.ticket;
   a.page_table = c.page_table;
   a.out = static_cast<uint16_t*>(c.out);
   a.lse = c.lse;
@@ -809,7 +806,7 @@ static cudaError_t run(const sa_geom& g, const ChunkCall& c, cudaStream_t stream
   if (e != cudaSuccess) return e;
   void* args[] = {&qm, &km, &vm, &a};
   if ((e = chunk_launch(fn, dim3(c.n_sm), kThreads, Y::kSmem, stream, args)) != cudaSuccess) return e;
-  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.shape.ticket, &a.out,
+  void* jargs[] = {&a.part_o, &a.part_ml, &a.cut, &a.out,
                    &a.lse,    &a.rows_cap, &a.Hq, &a.G, &a.TB};
   return chunk_launch(reinterpret_cast<const void*>(join_kernel<D>),
                       dim3(c.n_sm, a.rows_cap / 8), 256, 0, stream, jargs);

@@ -615,7 +615,6 @@ cudaError_t launch_chunk_mla(const sa_geom& g, const ChunkCall& c, cudaStream_t 
   a.shape.window = c.window < longest ? c.window : longest;
   a.shape.cap = (int64_t)g.max_pages * g.P;
   a.shape.status = c.status;
-  a.shape.ticket = nullptr;
   a.page_table = c.page_table;
   a.kv = static_cast<const uint8_t*>(c.k_cache);
   a.out = static_cast<uint16_t*>(c.out);

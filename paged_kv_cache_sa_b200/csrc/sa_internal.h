@@ -168,7 +168,6 @@ struct ChunkCall {
   float* lse;
   uint8_t* scratch;  // workspace behind the header, chunk_workspace_bytes
   int32_t* status;
-  int32_t* ticket;  // header word, zero between calls: the next whole item to hand out
   int n_sm;
 };
 size_t chunk_workspace_bytes(const sa_geom& g, int n_tokens, int n_sm);
