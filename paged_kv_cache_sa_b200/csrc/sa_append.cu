@@ -15,13 +15,17 @@
 //     read back from the cache, the new ones still in registers) need no atomics and no second
 //     launch.  A warp takes a KV head (latent rows: the CTA's row groups share the page).
 //   tokens: a run of rows of the call, as many as make about 1024 units; rotates their queries
-//     and copies their values.  Queries are most of the bytes (all of them in the latent
+//     and copies their values.  Queries are most of the bytes (nearly all in the latent
 //     geometry: 147 KB a token), so they are spread over the grid whatever the pages are, and
 //     their loads are in flight before the sequence and page of the rows are known.
 // cos/sin are computed once per CTA into shared memory and serve every head.  A lane holds a
 // "unit": two 16-byte chunks of one row that rotate together (j and j + rot/2 in the
 // half-split form, neighbours in the interleaved form), so loads and stores stay 16 bytes wide
 // and coalesced.  Bound by HBM: every row is read once and written once.
+// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 75.8 us (5.4 TB/s; the copy
+// reaches 6.5), 961 tokens of the latent geometry 59 us (4.8 TB/s), eight decode tokens 5 us
+// (latency: lengths, page table, keys and sine table one behind the other).  Runs of 2048 units
+// are 6% slower and of 512 13%, 128 threads a CTA 5% faster here but 25% slower for a decode step.
 #include "sa_common.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.h"
