@@ -46,17 +46,6 @@ constexpr int kSegs = 2;
 constexpr int kFirstKeys = 96;
 constexpr uint32_t kHalfBytes = kKeyTile * 128;  // 128 rows of 64 channels
 
-template <int D>
-struct Lay {
-  static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kRing = 2 * kTileBytes;
-  static constexpr uint32_t kMisc = kRing + kStages * kTileBytes;
-  static constexpr uint32_t kSmem = kMisc + 3072;
-};
-
 struct Misc {
   float2 ml[2][128];  // (m, l) of both chains, short blocks
   ChunkSeg seg[kSegs];
@@ -66,7 +55,18 @@ struct Misc {
   uint32_t tmem;
   int quit;
 };
-static_assert(sizeof(Misc) <= 3072, "misc area");
+
+template <int D>
+struct Lay {
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;  // a Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kRing = 2 * kTileBytes;
+  static constexpr uint32_t kMisc = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kSmem = kMisc + sizeof(Misc);
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
 
 struct Args {
   ChunkShape shape;

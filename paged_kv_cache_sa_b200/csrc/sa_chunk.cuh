@@ -265,7 +265,7 @@ struct ChunkSched {
     if (at >= items) return false;  // (so are those of all later rounds)
     const int t = (int)at;
 #pragma unroll 1
-    for (;; gb += 32) {
+    for (; gb < s.B; gb += 32) {
       int nn, LL;
       lane_seq(gb, nn, LL, false);
       const int mine = blocks(nn) * s.H;
@@ -278,12 +278,12 @@ struct ChunkSched {
         const int nb = __shfl_sync(0xffffffffu, mine, src) / s.H;
         h = q / nb;
         j = nb - 1 - (q - h * nb);
-        break;
+        chunk_seq(s, b, c0, n, L);
+        return true;
       }
       gpre += __shfl_sync(0xffffffffu, incl, 31);
     }
-    chunk_seq(s, b, c0, n, L);
-    return true;
+    return false;  // not reached unless sequences overlap and their blocks pass 32 bits
   }
 
   // The next piece; false when there is none.
