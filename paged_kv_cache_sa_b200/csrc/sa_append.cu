@@ -9,26 +9,38 @@
 // once, 2^-25 turns) goes to sincospif.  The rotation is fp32; the only rounding to bf16 is
 // the store.
 //
-// Two kinds of CTA in one launch:
+// Three kinds of CTA, two of them in a launch:
 //   pages: one CTA per (sequence, page that receives tokens).  The page is the unit that has a
 //     single owner, so the summaries (min/max over all valid rows of the page, the old ones
 //     read back from the cache, the new ones still in registers) need no atomics and no second
 //     launch.  A warp takes a KV head (latent rows: the CTA's row groups share the page).
-//   tokens: a run of rows of the call, as many as make about 1024 units; rotates their queries
-//     and copies their values.  Queries are most of the bytes (nearly all in the latent
-//     geometry: 147 KB a token), so they are spread over the grid whatever the pages are, and
-//     their loads are in flight before the sequence and page of the rows are known.
-// cos/sin are computed once per CTA into shared memory and serve every head.  A lane holds a
-// "unit": two 16-byte chunks of one row that rotate together (j and j + rot/2 in the
-// half-split form, neighbours in the interleaved form), so loads and stores stay 16 bytes wide
-// and coalesced.  Bound by HBM: every row is read once and written once.
-// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 75.8 us (5.4 TB/s; the copy
-// reaches 6.5), 961 tokens of the latent geometry 59 us (4.8 TB/s), eight decode tokens 5 us
+//   tokens (grouped-query geometry): a run of rows of the call, as many as make about 1024
+//     units; rotates their queries and copies their values.  Queries are most of the bytes, so
+//     they are spread over the grid whatever the pages are, and their loads are in flight
+//     before the sequence and page of the rows are known.
+//   queries (latent geometry): 147 KB a token, of which rotation concerns a ninth.  They pass
+//     through shared memory in bulk copies of 18 KB, three per CTA on their way in or out, and
+//     threads touch the rotated channels only.  (Through registers, as in the other geometry:
+//     59 us instead of 50 for 961 tokens, 11.6 instead of 6.5 us for 16.  The other geometry's
+//     queries through shared memory: 78 us instead of 73 for 16390 tokens, where every channel
+//     turns, and 15 instead of 12 us for 739 of which half of the channels turn.)
+// cos/sin are computed once per CTA (queries: once per token) into shared memory and serve every
+// head.  A "unit" is two 16-byte chunks of one row that rotate together (j and j + rot/2 in the
+// half-split form, neighbours in the interleaved form); a thread keeps its unit's place and
+// walks the rows, so that loads and stores stay 16 bytes wide and coalesced and little is spent
+// on addresses (a count through all units of a run instead: 76 us for the 16390 tokens).
+// Bound by HBM: every row is read once and written once.
+// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 71.6 us (5.7 TB/s; the copy
+// reaches 6.5), 961 tokens of the latent geometry 50.3 us (5.7 TB/s), eight decode tokens 5 us
 // (latency: lengths, page table, keys and sine table one behind the other).  Runs of 2048 units
-// are 6% slower and of 512 13%, 128 threads a CTA 5% faster here but 25% slower for a decode step.
+// are 6% slower and of 512 13%, 128 threads a CTA 5% faster here but 25% slower for a decode
+// step.  Latent pieces of 30 KB, four stages or fewer and larger CTAs: 1 to 7% slower.
+#include <algorithm>
+
 #include "sa_common.cuh"
 #include "sa_fp8.cuh"
 #include "sa_internal.h"
+#include "sa_tc.cuh"
 
 namespace sa {
 
@@ -36,8 +48,15 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kMaxRun = 64;     // tokens of a token CTA, at most
-constexpr int kRunUnits = 1024; // query units that a token CTA is sized for
+constexpr int kMaxRun = 64;      // tokens of a token CTA, at most
+constexpr int kRunUnits = 1024;  // query units that a token CTA is sized for
+constexpr int kMaxKnown = 16;    // tokens that a query CTA looks up at a time
+constexpr int kHeads = 16;       // latent heads of a piece
+constexpr uint32_t kPieceBytes = kHeads * 576 * 2;
+constexpr int kStages = 3;       // pieces in a query CTA's shared memory
+constexpr int kQueryCtas = 3;    // query CTAs of an SM
+constexpr int kLatentGroups = kAppendThreads / 36;  // thread groups that share a latent page's rows
+static_assert(kMaxKnown <= kMaxRun, "Tokens");
 
 struct AppendArgs {
   const uint4* q;
@@ -57,10 +76,23 @@ struct AppendArgs {
   int n_tokens, B, Hq, Hkv, P, max_pages, n_pool;
   int rot_start, rot_dim, interleaved;
   int want;  // 0: no summaries, 1: bf16 rows, 2: fp8 records
-  int n_page_ctas, run;    // CTAs of the first kind; tokens of a CTA of the second
-  uint32_t per_q, per_v;   // units of a token's queries, chunks of its values
-  uint32_t inv_q, inv_v;   // ceil(2^32 / per): e / per = mulhi(e, inv) while e * per < 2^32
+  int n_query_ctas, n_page_ctas;  // latent queries' CTAs come first, then the pages'
+  int run;                        // tokens of a token CTA
+  uint32_t inv_half, inv_hq, inv_hkv;  // see quot(), of rot_dim / 2 and counts of heads
 };
+
+// e / d where inv = ceil(2^32 / d) and e * d < 2^32
+__device__ __forceinline__ uint32_t quot(uint32_t e, uint32_t d, uint32_t inv) {
+  return d == 1 ? e : __umulhi(e, inv);
+}
+
+// shared memory -> global, as part of this thread's current group of copies
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
 
 // the two chunks of unit u of a row, and the place of its first rotation pair (-1: not rotated)
 struct Unit {
@@ -190,16 +222,17 @@ __device__ __forceinline__ float2 cos_sin(int pos, float f) {
 
 // CPR = 16-byte chunks per key row (Dk / 8).
 template <int CPR>
-__device__ __forceinline__ void append_pages(const AppendArgs& a, float2* cs) {
+__device__ __forceinline__ void append_pages(const AppendArgs& a, uint8_t* smem, int cta) {
   constexpr int U = CPR / 2;  // units per row
   __shared__ int scan[kAppendWarps];
   __shared__ int found[2];  // sequence and page of this CTA's item
+  float2* cs = reinterpret_cast<float2*>(smem);  // [tokens][rot_dim / 2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = a.rot_dim >> 1;
   const bool inter = a.interleaved != 0;
   const int64_t cap = (int64_t)a.max_pages * a.P;
 
-  for (int item = blockIdx.x;; item += a.n_page_ctas) {
+  for (int item = cta;; item += a.n_page_ctas) {
     // ---- the item's sequence and page: running count of touched pages over the batch
     if (tid == 0) found[0] = -1;
     int before = 0;
@@ -255,7 +288,7 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, float2* cs) {
     const int pos0 = (a.logical_lens ? a.logical_lens[b] : L) - n + (t0 - s0);
     // ---- cos and sin of every (new token, pair)
     for (int e = tid; e < cnt * half; e += kAppendThreads) {
-      const int i = e / half, j = e - i * half;
+      const int i = quot(e, half, a.inv_half), j = e - i * half;
       cs[i * half + pair_at(j, half)] = cos_sin(pos0 + i, a.inv_freq[j]);
     }
     __syncthreads();
@@ -331,8 +364,8 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, float2* cs) {
     } else {
       // latent rows (one KV head): the CTA's row groups split the page's rows, their
       // partial ranges meet in shared memory
-      constexpr int NG = kAppendThreads / U - 1;  // (shared memory: one group of threads rests)
-      __shared__ Range part[NG][CPR];
+      constexpr int NG = kLatentGroups;
+      Range(*part)[CPR] = reinterpret_cast<Range(*)[CPR]>(smem + a.P * half * sizeof(float2));
       const int u = tid % U, rg = tid / U;
       const Unit x = unit_of<CPR>(u, a.rot_start, a.rot_dim, inter);
       uint4* blk = a.k_cache + (size_t)phys * a.P * CPR;
@@ -379,103 +412,200 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, float2* cs) {
   }
 }
 
-// Tokens [r0, r0 + run) of the call: queries rotated, values to their slots.
+// Where tokens of the call belong.
+struct Tokens {
+  int seq[kMaxRun], slot[kMaxRun], pos[kMaxRun];  // slot: in its page
+  int page[kMaxRun];                              // -1: belongs to no sequence or no page
+
+  // tokens [r0, r0 + cnt), by the whole CTA; a barrier follows before they are read
+  __device__ __forceinline__ void find(const AppendArgs& a, int r0, int cnt) {
+    const int tid = threadIdx.x;
+    const int64_t cap = (int64_t)a.max_pages * a.P;
+    if (tid < kMaxRun) page[tid] = -1;
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kAppendThreads) {
+      int c0, n, L;
+      new_tokens(a.cu_new, a.seq_lens, b, a.n_tokens, cap, a.status, c0, n, L);
+      const int i0 = max(c0, r0), i1 = min(c0 + n, r0 + cnt);
+      if (i0 < i1) {
+        const int p = (a.logical_lens ? a.logical_lens[b] : L) - n - c0;
+        for (int i = i0; i < i1; ++i) {
+          seq[i - r0] = b;
+          slot[i - r0] = L - n + i - c0;
+          pos[i - r0] = p + i;
+          page[i - r0] = 0;
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < cnt && page[tid] == 0) {
+      const int lp = slot[tid] / a.P;
+      const int phys = a.page_table[(size_t)seq[tid] * a.max_pages + lp];
+      const bool ok = phys >= 0 && phys < a.n_pool;
+      if (!ok) report(a.status, SA_ERR_DEVICE_CHECK);
+      page[tid] = ok ? phys : -1;
+      slot[tid] -= lp * a.P;
+    }
+  }
+};
+
+// Tokens [r0, r0 + run) of the call: queries rotated, values to their slots.  A row is a head of a
+// token; a thread keeps its place in the rows, one unit of four neighbouring ones.
 template <int CPR>
 __device__ __forceinline__ void append_tokens(const AppendArgs& a, float2* cs, int r0) {
-  constexpr int U = CPR / 2;
-  __shared__ int t_seq[kMaxRun], t_slot[kMaxRun], t_pos[kMaxRun], t_row[kMaxRun];
+  __shared__ Tokens tok;
+  constexpr int U = CPR / 2, N = 4;  // units of a row, rows of a thread
   const int tid = threadIdx.x;
   const int half = a.rot_dim >> 1;
   const bool inter = a.interleaved != 0;
-  const int64_t cap = (int64_t)a.max_pages * a.P;
   const int cnt = min(a.run, a.n_tokens - r0);
-  // queries of four units per thread at a time; the first four's loads start here
-  const uint32_t n_q = a.q ? cnt * a.per_q : 0;
-  uint4 va[4], vb[4];
-  auto fetch = [&](uint32_t e0) {
+  const int rows = a.q ? cnt * a.Hq : 0;
+  const uint4* src = a.q + (size_t)r0 * a.q_stride;
+  const int64_t skip = a.q_stride - (int64_t)a.Hq * CPR;  // between tokens, past their rows
+  uint4* dst = a.q_out + (size_t)r0 * a.Hq * CPR;
+  const Unit y = unit_of<CPR>(tid % U, a.rot_start, a.rot_dim, inter);
+  const int first = tid / U;
+  constexpr int step = kAppendThreads / U * N;
+  uint4 va[N], vb[N];
+  auto fetch = [&](int row0) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t e = e0 + x * kAppendThreads;
-      if (e < n_q) {
-        const uint32_t i = a.per_q == 1 ? e : __umulhi(e, a.inv_q), w = e - i * a.per_q;
-        const Unit y = unit_of<CPR>(w % U, a.rot_start, a.rot_dim, inter);
-        const uint4* src = a.q + (size_t)(r0 + i) * a.q_stride + w / U * CPR;
-        va[x] = src[y.ca];
-        vb[x] = src[y.cb];
+    for (int k = 0; k < N; ++k) {
+      const int row = row0 + k * (kAppendThreads / U);
+      if (row < rows) {
+        const uint4* p = src + (row * CPR + quot(row, a.Hq, a.inv_hq) * skip);
+        va[k] = p[y.ca];
+        vb[k] = p[y.cb];
       }
     }
   };
-  fetch(tid);
-  if (tid < kMaxRun) t_row[tid] = -1;
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kAppendThreads) {
-    int c0, n, L;
-    new_tokens(a.cu_new, a.seq_lens, b, a.n_tokens, cap, a.status, c0, n, L);
-    const int i0 = max(c0, r0), i1 = min(c0 + n, r0 + cnt);
-    if (i0 < i1) {
-      const int pos = (a.logical_lens ? a.logical_lens[b] : L) - n - c0;
-      for (int i = i0; i < i1; ++i) {
-        t_seq[i - r0] = b;
-        t_slot[i - r0] = L - n + i - c0;
-        t_pos[i - r0] = pos + i;
-        t_row[i - r0] = 0;
-      }
-    }
-  }
-  __syncthreads();
-  // row of the token in the pool (page * P + slot), -1: belongs to no sequence or no page
-  if (tid < cnt && t_row[tid] == 0) {
-    const int lp = t_slot[tid] / a.P;
-    const int phys = a.page_table[(size_t)t_seq[tid] * a.max_pages + lp];
-    const bool ok = phys >= 0 && phys < a.n_pool;
-    if (!ok) report(a.status, SA_ERR_DEVICE_CHECK);
-    t_row[tid] = ok ? phys : -1;
-    t_slot[tid] -= lp * a.P;
-  }
+  fetch(first);  // before it is known where the tokens belong
+  tok.find(a, r0, cnt);
   for (int e = tid; e < (a.q ? cnt * half : 0); e += kAppendThreads) {
-    const int i = e / half, j = e - i * half;
-    cs[i * half + pair_at(j, half)] = cos_sin(t_pos[i], a.inv_freq[j]);
+    const int i = quot(e, half, a.inv_half), j = e - i * half;
+    cs[i * half + pair_at(j, half)] = cos_sin(tok.pos[i], a.inv_freq[j]);
   }
   __syncthreads();
-  for (uint32_t e0 = tid; e0 < n_q; e0 += 4 * kAppendThreads) {
-    if (e0 != tid) fetch(e0);
+  for (int row0 = first; row0 < rows; row0 += step) {
+    if (row0 != first) fetch(row0);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t e = e0 + x * kAppendThreads;
-      const uint32_t i = a.per_q == 1 ? e : __umulhi(e, a.inv_q), w = e - i * a.per_q;
-      if (e < n_q && t_row[i] >= 0) {
-        const Unit y = unit_of<CPR>(w % U, a.rot_start, a.rot_dim, inter);
-        if (y.pair >= 0) rotate_unit(va[x], vb[x], cs + i * half + y.pair, half, inter);
-        uint4* dst = a.q_out + ((size_t)(r0 + i) * a.Hq + w / U) * CPR;
-        dst[y.ca] = va[x];
-        dst[y.cb] = vb[x];
+    for (int k = 0; k < N; ++k) {
+      const int row = row0 + k * (kAppendThreads / U);
+      const int i = quot(row, a.Hq, a.inv_hq);
+      if (row < rows && tok.page[i] >= 0) {
+        if (y.pair >= 0) rotate_unit(va[k], vb[k], cs + i * half + y.pair, half, inter);
+        dst[row * CPR + y.ca] = va[k];
+        dst[row * CPR + y.cb] = vb[k];
       }
     }
   }
-  const uint32_t n_v = a.v ? cnt * a.per_v : 0;
+  // values: chunk vc of rows vy, vy + vp, ...
+  constexpr int vp = kAppendThreads / CPR;
+  const int vy = tid / CPR, vc = tid % CPR;
+  const int v_rows = cnt * a.Hkv;
+  const uint4* vsrc = a.v + (size_t)r0 * a.v_stride + vc;
 #pragma unroll 4
-  for (uint32_t e = tid; e < n_v; e += kAppendThreads) {
-    const uint32_t i = a.per_v == 1 ? e : __umulhi(e, a.inv_v), w = e - i * a.per_v;
-    const int phys = t_row[i];
-    const uint4 x = a.v[(size_t)(r0 + i) * a.v_stride + w];
+  for (int row = vy; row < v_rows; row += vp) {
+    const int i = quot(row, a.Hkv, a.inv_hkv), h = row - i * a.Hkv;
+    const int phys = tok.page[i];
+    const uint4 w = vsrc[i * a.v_stride + h * CPR];
     if (phys >= 0)
-      a.v_cache[(((size_t)phys * a.Hkv + w / CPR) * a.P + t_slot[i]) * CPR + w % CPR] = x;
+      a.v_cache[(((size_t)phys * a.Hkv + h) * a.P + tok.slot[i]) * CPR + vc] = w;
   }
   __syncthreads();  // the shared arrays are free for the next run
 }
 
+// Queries of the latent geometry, a range of pieces (kHeads heads of a token) per CTA: a piece
+// comes into shared memory as one bulk copy, its few rotated channels are turned there, and it
+// leaves as one; the other eight ninths are never touched by a thread.  Meanwhile the next
+// pieces are on their way in and the last one is on its way out.
+__device__ __forceinline__ void append_queries(const AppendArgs& a, uint8_t* smem) {
+  constexpr int CPR = 72, kParts = 128 / kHeads;
+  __shared__ uint64_t full[kStages];
+  __shared__ Tokens tok;  // of tokens [known, known + kMaxKnown)
+  __shared__ int quit;
+  float2* cs = reinterpret_cast<float2*>(smem + kStages * kPieceBytes);
+  const int tid = threadIdx.x;
+  const int half = a.rot_dim >> 1, n_rot = a.rot_dim >> 4;
+  const bool inter = a.interleaved != 0;
+  const int64_t pieces = (int64_t)a.n_tokens * kParts;
+  const int64_t p0 = pieces * blockIdx.x / a.n_query_ctas;
+  const int np = (int)(pieces * (blockIdx.x + 1) / a.n_query_ctas - p0);
+  auto load = [&](int n) {  // piece n of this CTA; one thread
+    const int64_t p = p0 + n;
+    mbar_arrive_expect_tx(&full[n % kStages], kPieceBytes);
+    bulk_load(smem + n % kStages * kPieceBytes,
+              a.q + (p / kParts) * a.q_stride + (p % kParts) * (kHeads * CPR), kPieceBytes,
+              &full[n % kStages]);
+  };
+  if (tid == 0) {
+    quit = 0;
+    for (int x = 0; x < kStages; ++x) mbar_init(&full[x], 1);
+    fence_mbar_init();
+    for (int n = 0; n < min(np, kStages); ++n) load(n);
+  }
+  int known = -1, turned = -1;  // first of the known tokens, token that cs is of
+  const int h = n_rot ? tid / n_rot : kHeads;  // this thread's head and unit
+  const Unit y = unit_of<CPR>(n_rot ? tid % n_rot : 0, a.rot_start, a.rot_dim, inter);
+  int n = 0;
+  for (; n < np; ++n) {
+    const int r = (int)((p0 + n) / kParts), part = (int)((p0 + n) % kParts);
+    if (known < 0 || r >= known + kMaxKnown) {
+      __syncthreads();  // (quit and the barriers are set up; tok was read)
+      known = r;
+      tok.find(a, known, min(kMaxKnown, a.n_tokens - known));
+    }
+    if (turned != r) {
+      turned = r;
+      for (int j = tid; j < half; j += kAppendThreads)
+        cs[pair_at(j, half)] = cos_sin(tok.pos[r - known], a.inv_freq[j]);
+    }
+    __syncthreads();
+    uint4* buf = reinterpret_cast<uint4*>(smem + n % kStages * kPieceBytes);
+    const bool here = tc::wait(&full[n % kStages], (n / kStages) & 1, &quit, a.status);
+    if (here) {
+      for (int row = h; row < kHeads; row += kAppendThreads / n_rot) {
+        uint4 va = buf[row * CPR + y.ca], vb = buf[row * CPR + y.cb];
+        rotate_unit(va, vb, cs + y.pair, half, inter);
+        buf[row * CPR + y.ca] = va;
+        buf[row * CPR + y.cb] = vb;
+      }
+      tc::fence_async_smem();
+    }
+    if (!__syncthreads_and(here)) break;
+    if (tid == 0) {
+      if (tok.page[r - known] >= 0)
+        bulk_store(a.q_out + ((size_t)r * 128 + part * kHeads) * CPR, buf, kPieceBytes);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      if (n > 0 && n - 1 + kStages < np) {  // into the stage of the piece before this one
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        load(n - 1 + kStages);
+      }
+    }
+  }
+  if (tid == 0) {
+    // nothing is on its way when the CTA ends (n < np: a wait ran out)
+    for (int i = n; i < min(np, n == 0 ? kStages : n - 1 + kStages); ++i)
+      mbar_wait(&full[i % kStages], (i / kStages) & 1);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+}
+
 template <int CPR>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendArgs a) {
-  extern __shared__ __align__(16) float2 cs[];  // [tokens][rot_dim / 2]
+__global__ void __launch_bounds__(kAppendThreads, CPR == 72 ? 3 : 4)
+append_kernel(const AppendArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
   if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x < a.n_page_ctas) {
-    append_pages<CPR>(a, cs);
+  const int cta = blockIdx.x - a.n_query_ctas;
+  if (cta >= 0 && cta < a.n_page_ctas) {
+    append_pages<CPR>(a, smem, cta);
+  } else if constexpr (CPR == 72) {
+    append_queries(a, smem);
   } else {
-    const int64_t step = (int64_t)(gridDim.x - a.n_page_ctas) * a.run;
-    for (int64_t r0 = (int64_t)(blockIdx.x - a.n_page_ctas) * a.run; r0 < a.n_tokens; r0 += step)
-      append_tokens<CPR>(a, cs, (int)r0);
+    const int64_t step = (int64_t)(gridDim.x - a.n_query_ctas - a.n_page_ctas) * a.run;
+    for (int64_t r0 = (int64_t)(cta - a.n_page_ctas) * a.run; r0 < a.n_tokens; r0 += step)
+      append_tokens<CPR>(a, reinterpret_cast<float2*>(smem), (int)r0);
   }
 }
 
@@ -517,16 +647,29 @@ cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t st
   if (items > c.n_tokens) items = c.n_tokens;
   if (items > 1 << 20) items = 1 << 20;  // the kernel strides over the rest
   a.n_page_ctas = (int)items;
-  a.per_q = g.Hq * (g.Dk / 16);
-  a.per_v = g.Hkv * (g.Dv / 8);
-  a.inv_q = (uint32_t)(((1ull << 32) + a.per_q - 1) / a.per_q);
-  a.inv_v = (uint32_t)(((1ull << 32) + a.per_v - 1) / a.per_v);
-  a.run = kRunUnits / (int)a.per_q;
-  a.run = a.run < 1 ? 1 : a.run > kMaxRun ? kMaxRun : a.run;
-  int64_t runs = a.q || a.v ? ((int64_t)c.n_tokens + a.run - 1) / a.run : 0;
-  if (runs > 1 << 20) runs = 1 << 20;
-  // cos and sin of a page's or a run's tokens: at most 32 KB
-  const size_t smem = (size_t)(g.P > a.run ? g.P : a.run) * (c.rot_dim / 2) * sizeof(float2);
+  auto inv = [](int d) { return d ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0; };
+  a.inv_half = inv(c.rot_dim / 2);
+  a.inv_hq = inv(g.Hq);
+  a.inv_hkv = inv(g.Hkv);
+  // cos and sin of the tokens of a page or a run: at most 32 KB
+  const size_t table = (size_t)(c.rot_dim / 2) * sizeof(float2);
+  size_t smem = g.P * table;
+  int64_t runs = 0;
+  a.n_query_ctas = 0;
+  if (g.Dk != 576) {
+    a.run = kRunUnits / (g.Hq * (g.Dk / 16));
+    a.run = a.run < 1 ? 1 : a.run > kMaxRun ? kMaxRun : a.run;
+    runs = ((int64_t)c.n_tokens + a.run - 1) / a.run;
+    if (runs > 1 << 20) runs = 1 << 20;
+    if (a.q) smem = std::max(smem, a.run * table);
+  } else {
+    smem += kLatentGroups * 72 * sizeof(Range);
+    if (a.q) {
+      a.n_query_ctas = (int)std::min<int64_t>((int64_t)c.n_tokens * (128 / kHeads),
+                                              kQueryCtas * c.n_sm);
+      smem = std::max(smem, kStages * kPieceBytes + table);
+    }
+  }
   const void* fn;
   switch (g.Dk) {
     case 64: fn = reinterpret_cast<const void*>(append_kernel<8>); break;
@@ -535,7 +678,10 @@ cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t st
     default: return cudaErrorInvalidValue;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items + runs));
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kStages * kPieceBytes + 32768);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(a.n_query_ctas + items + runs));
   cfg.blockDim = dim3(kAppendThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -664,6 +664,7 @@ SA_EXPORT int sa_append_kv(const sa_geom* g, const void* q, int64_t q_stride, co
   c.summ = summ;
   c.summ8 = summ8;
   c.status = &static_cast<WsHeader*>(ws)->status_bits;
+  c.n_sm = sm_count();
   return cuda_status(launch_append(*g, c, static_cast<cudaStream_t>(stream)));
 }
 

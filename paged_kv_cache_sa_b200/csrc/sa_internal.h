@@ -150,6 +150,7 @@ struct AppendCall {
   void* summ;   // bf16 summaries (nullable)
   void* summ8;  // fp8 records (nullable)
   int32_t* status;
+  int n_sm;
 };
 cudaError_t launch_append(const sa_geom& g, const AppendCall& c, cudaStream_t stream);
 

@@ -175,6 +175,59 @@ def test_rotation_in_place():
 
 
 @gpu
+@pytest.mark.parametrize("interleaved,rot,start,in_place", [
+    (True, 64, 512, False), (False, 64, 512, True), (False, 48, 40, False)])
+def test_latent_queries_of_many_tokens(interleaved, rot, start, in_place):
+    """More tokens than the CTAs look up at a time; rows apart from one another or rotated in
+    place; a sequence whose page is bad and rows of no sequence stay as they were."""
+    new = [2500, 0, 1, 3000, 7, 1700] + [5] * 20
+    b = Batch("latent", new, [n + 11 * i for i, n in enumerate(new)], pad=9, seed=rot)
+    g, bad = b.g, 4
+    table = b.table.clone()
+    table[bad] = -1
+    gen = torch.Generator("cuda").manual_seed(1)
+    big = torch.randn(b.n, 128 + (0 if in_place else 1), 576, device="cuda", generator=gen,
+                      dtype=torch.bfloat16)
+    q, k = big[:, :128], b.normal(b.n, 1, 576).cuda()
+    before = q.clone()
+    q_out = q if in_place else torch.full((b.n, 128, 576), 3.0, dtype=torch.bfloat16,
+                                          device="cuda")
+    was = q_out[-1:].clone() if not in_place else None
+    ws = sa.Workspace.for_chunk(g, b.n)
+    inv = freq(rot)
+    sa.append_kv(g, k, None, b.to(b.cu), b.to(table), b.to(b.seq), b.to(b.k_cache), None, ws,
+                 q=q, q_out=q_out, inv_freq=inv.cuda(), rot_start=start, interleaved=interleaved)
+    assert ws.status() == sa.SA_ERR_DEVICE_CHECK
+    at = 0
+    for i, (n, L) in enumerate(zip(new, b.lens)):
+        for lo in range(0, n, 500):
+            r = slice(at + lo, at + min(lo + 500, n))
+            if i == bad:
+                want = before[r] if in_place else was.expand(r.stop - r.start, -1, -1)
+                assert torch.equal(q_out[r], want)
+                continue
+            pos = torch.arange(r.start, r.stop, device="cuda") - at + L - n
+            half = rot // 2
+            j = torch.arange(half, device="cuda")
+            first = start + (2 * j if interleaved else j)
+            second = first + (1 if interleaved else half)
+            angle = torch.outer(pos.double(), inv.double().cuda())[:, None]
+            c, sn = angle.cos(), angle.sin()
+            x = before[r].double()
+            u, w = x[..., first], x[..., second]
+            got = q_out[r].double()
+            for ch, want in ((first, u * c - w * sn), (second, w * c + u * sn)):
+                tol = HALF_STEP * want.abs() + 2.0 ** -20 * (u.abs() + w.abs())
+                assert bool(((got[..., ch] - want).abs() <= tol).all())
+            rest = torch.ones(576, dtype=torch.bool, device="cuda")
+            rest[first] = rest[second] = False
+            assert torch.equal(got[..., rest], x[..., rest])
+        at += n
+    want = before[at:] if in_place else was.expand(b.n - at, -1, -1)
+    assert torch.equal(q_out[at:], want)
+
+
+@gpu
 def test_bad_pages_and_lengths_are_reported_and_left_out():
     b = Batch("tiny", [20, 3, 1], [40, 3, 9], pad=1, seed=11)
     g = b.g
