@@ -30,7 +30,7 @@
 // walks the rows, so that loads and stores stay 16 bytes wide and coalesced and little is spent
 // on addresses (a count through all units of a run instead: 76 us for the 16390 tokens).
 // Bound by HBM: every row is read once and written once.
-// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 71.6 us (5.7 TB/s; the copy
+// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 70.5 us (5.8 TB/s; the copy
 // reaches 6.5), 961 tokens of the latent geometry 50.3 us (5.7 TB/s), eight decode tokens 5 us
 // (latency: lengths, page table, keys and sine table one behind the other).  Runs of 2048 units
 // are 6% slower and of 512 13%, 128 threads a CTA 5% faster here but 25% slower for a decode
@@ -286,6 +286,29 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, uint8_t* smem,
       continue;
     }
     const int pos0 = (a.logical_lens ? a.logical_lens[b] : L) - n + (t0 - s0);
+    const int rows = slot0 + cnt;
+    const int from = a.want ? 0 : slot0;
+    // keys of a lane's rows r, r + RPW, ...: old ones from the cache, new ones from the call; the
+    // first two are on their way while the angles are computed (four: the registers overflow)
+    constexpr bool grouped = 32 % U == 0;
+    constexpr int RPW = grouped ? 32 / U : 1, N = 2;
+    const int u = grouped ? lane % U : tid % U, rg = grouped ? lane / U : tid / U;
+    const Unit x = unit_of<CPR>(u, a.rot_start, a.rot_dim, inter);
+    uint4 va[N], vb[N];
+    auto fetch = [&](int h, int r0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int r = r0 + k * RPW;
+        if (r < rows) {
+          const uint4* src = r < slot0
+                                 ? a.k_cache + (((size_t)phys * a.Hkv + h) * a.P + r) * CPR
+                                 : a.k + (size_t)(row0 + r - slot0) * a.k_stride + h * CPR;
+          va[k] = src[x.ca];
+          vb[k] = src[x.cb];
+        }
+      }
+    };
+    if (grouped && warp < a.Hkv) fetch(warp, from + rg);
     // ---- cos and sin of every (new token, pair)
     for (int e = tid; e < cnt * half; e += kAppendThreads) {
       const int i = quot(e, half, a.inv_half), j = e - i * half;
@@ -294,34 +317,27 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, uint8_t* smem,
     __syncthreads();
 
     // ---- keys: rotate and store the new rows, min/max over the page's valid rows
-    const int rows = slot0 + cnt;
-    const int from = a.want ? 0 : slot0;
-    if constexpr (32 % U == 0) {
-      const int u = lane % U, rg = lane / U;
-      constexpr int RPW = 32 / U;
-      const Unit x = unit_of<CPR>(u, a.rot_start, a.rot_dim, inter);
+    if constexpr (grouped) {
       for (int h = warp; h < a.Hkv; h += kAppendWarps) {
         uint4* blk = a.k_cache + ((size_t)phys * a.Hkv + h) * a.P * CPR;
         Range ra, rb;
         ra.clear();
         rb.clear();
-#pragma unroll 4
-        for (int r = from + rg; r < rows; r += RPW) {
-          uint4 va, vb;
-          if (r < slot0) {
-            va = blk[r * CPR + x.ca];
-            vb = blk[r * CPR + x.cb];
-          } else {
-            const int i = r - slot0;
-            const uint4* src = a.k + (size_t)(row0 + i) * a.k_stride + h * CPR;
-            va = src[x.ca];
-            vb = src[x.cb];
-            if (x.pair >= 0) rotate_unit(va, vb, cs + i * half + x.pair, half, inter);
-            blk[r * CPR + x.ca] = va;
-            blk[r * CPR + x.cb] = vb;
+        for (int r0 = from + rg; r0 < rows; r0 += N * RPW) {
+          if (h != warp || r0 != from + rg) fetch(h, r0);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int r = r0 + k * RPW;
+            if (r >= rows) break;
+            if (r >= slot0) {
+              if (x.pair >= 0)
+                rotate_unit(va[k], vb[k], cs + (r - slot0) * half + x.pair, half, inter);
+              blk[r * CPR + x.ca] = va[k];
+              blk[r * CPR + x.cb] = vb[k];
+            }
+            ra.add(va[k]);
+            rb.add(vb[k]);
           }
-          ra.add(va);
-          rb.add(vb);
         }
         if (a.want) {
 #pragma unroll
@@ -366,8 +382,6 @@ __device__ __forceinline__ void append_pages(const AppendArgs& a, uint8_t* smem,
       // partial ranges meet in shared memory
       constexpr int NG = kLatentGroups;
       Range(*part)[CPR] = reinterpret_cast<Range(*)[CPR]>(smem + a.P * half * sizeof(float2));
-      const int u = tid % U, rg = tid / U;
-      const Unit x = unit_of<CPR>(u, a.rot_start, a.rot_dim, inter);
       uint4* blk = a.k_cache + (size_t)phys * a.P * CPR;
       Range ra, rb;
       ra.clear();
