@@ -177,9 +177,8 @@ struct ChunkSched {
     lane_h = s.inner == 1 ? 0 : cta % s.inner;
     runs = s.inner == 1 ? n_cta : n_cta / s.inner;
     const int lane = threadIdx.x & 31;
-    uint64_t all = 0;
+    uint64_t all = 0, count = 0;
     uint32_t longest = 0, mine = 0;
-    items = 0;
 #pragma unroll 1
     for (int base = 0; base < s.B; base += 32) {
       int nn, LL;
@@ -188,11 +187,16 @@ struct ChunkSched {
       mine = seq_cost(nn, LL, mx);
       all += __reduce_add_sync(0xffffffffu, mine & 0xFFFFu) +
              ((uint64_t)__reduce_add_sync(0xffffffffu, mine >> 16) << 16);
-      items += __reduce_add_sync(0xffffffffu, blocks(nn));
+      count += __reduce_add_sync(0xffffffffu, blocks(nn));
       longest = max(longest, __reduce_max_sync(0xffffffffu, mx));
     }
     all *= s.H;
-    items *= s.H;
+    // (more items than that only if sequences overlap; next_whole() counts in 32 bits)
+    if (count * s.H >> 31) {
+      all = 0;
+      if (cta == 0) report(s.status, SA_ERR_DEVICE_CHECK);
+    }
+    items = (int)(count * s.H);
     // whole items, too, where a count of steps would not fit 32 bits
     whole = all >= (uint64_t)kWholeFactor * longest * runs || all >> 31;
     left = 0;
@@ -265,7 +269,7 @@ struct ChunkSched {
     if (at >= items) return false;  // (so are those of all later rounds)
     const int t = (int)at;
 #pragma unroll 1
-    for (; gb < s.B; gb += 32) {
+    for (;; gb += 32) {
       int nn, LL;
       lane_seq(gb, nn, LL, false);
       const int mine = blocks(nn) * s.H;
@@ -278,12 +282,12 @@ struct ChunkSched {
         const int nb = __shfl_sync(0xffffffffu, mine, src) / s.H;
         h = q / nb;
         j = nb - 1 - (q - h * nb);
-        chunk_seq(s, b, c0, n, L);
-        return true;
+        break;
       }
       gpre += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return false;  // not reached unless sequences overlap and their blocks pass 32 bits
+    chunk_seq(s, b, c0, n, L);
+    return true;
   }
 
   // The next piece; false when there is none.
