@@ -102,10 +102,12 @@ struct Loader {
   uint32_t smem;
   Misc& mi;
   const CUtensorMap* map;
+  bool values;  // V's
   int lane, ppt, my_page, my_half;
 
-  __device__ __forceinline__ Loader(const Args& args, uint32_t s, Misc& m, const CUtensorMap* mp)
-      : a(args), smem(s), mi(m), map(mp) {
+  __device__ __forceinline__ Loader(const Args& args, uint32_t s, Misc& m, const CUtensorMap* mp,
+                                    bool v)
+      : a(args), smem(s), mi(m), map(mp), values(v) {
     lane = threadIdx.x & 31;
     ppt = kKeyTile >> a.page_shift;  // pages per tile
     my_page = lane & (ppt - 1);
@@ -113,7 +115,6 @@ struct Loader {
   }
 
   // Tiles of one piece; a lane copies one page's rows of one half of the channels.
-  template <bool V>
   __device__ __forceinline__ bool tiles(const ChunkSeg& g) {
     const int nt = g.i1 - g.i0, shift = a.page_shift;
     const int s_hi = g.s0 + g.ntok - 1, last_page = (g.L - 1) >> shift;
@@ -134,7 +135,7 @@ struct Loader {
     for (int i = -3; i < nt; ++i) {
       const int p3 = i + 3 < nt && wanted(i + 3, lp) ? row[lp] : -1;
       if (i >= 0) {
-        const int x = g.it0 + (V ? v_pos(g.split, nt, i) : k_pos(g.split, i));
+        const int x = g.it0 + (values ? v_pos(g.split, nt, i) : k_pos(g.split, i));
         const int st = x % Y::kStages;
         bool copy = wanted(i, lp);
         if (copy && (p0 < 0 || p0 >= a.n_pool)) {
@@ -166,63 +167,61 @@ struct Loader {
   }
 };
 
+// Both warps run the same code: the kernel is larger than its instruction cache, and a copy each
+// is 1% slower on long chunks and 3% on short prompts (6 x 2368 rows 278 -> 270 us).
 template <int D>
-__device__ __forceinline__ void produce_k(const Args& a, uint32_t smem, Misc& mi,
-                                          const CUtensorMap* qmap, const CUtensorMap* kmap) {
+__device__ __forceinline__ void produce(const Args& a, uint32_t smem, Misc& mi,
+                                        const CUtensorMap* qmap, const CUtensorMap* map,
+                                        bool values) {
   using Y = Lay<D>;
-  Loader<D> load(a, smem, mi, kmap);
+  Loader<D> load(a, smem, mi, map, values);
   const int lane = load.lane;
   ChunkSched sched;
-  if (lane == 0) a.cut[blockIdx.x].nparts = 0;
-  sched.init(a.shape, blockIdx.x, gridDim.x);
+  if (!values) {
+    if (lane == 0) a.cut[blockIdx.x].nparts = 0;
+    sched.init(a.shape, blockIdx.x, gridDim.x);
+  }
   int it = 0;
+#pragma unroll 1
   for (int n = 0;; ++n) {
     const int slot = n % kSegs;
-    if (n >= kSegs && !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit,
-                                     a.shape.status))
-      break;
     ChunkSeg g;
-    const bool more = sched.next(g);
-    if (!more) g.valid = 0;
-    g.it0 = it;
-    if (lane == 0) {
-      mi.seg[slot] = g;
-      mbar_arrive(&mi.seg_full[slot]);
-      if (more && g.nparts > 0) a.cut[blockIdx.x] = ChunkCut{g.nparts, g.row0, g.ntok, g.h};
+    if (values) {
+      if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, a.shape.status)) break;
+      g = mi.seg[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mi.seg_empty[slot]);
+      if (!g.valid) return;
+    } else {
+      if (n >= kSegs && !tc::wait_warp(&mi.seg_empty[slot], (n / kSegs - 1) & 1, &mi.quit,
+                                       a.shape.status))
+        break;
+      const bool more = sched.next(g);
+      if (!more) g.valid = 0;
+      g.it0 = it;
+      if (lane == 0) {
+        mi.seg[slot] = g;
+        mbar_arrive(&mi.seg_full[slot]);
+        if (more && g.nparts > 0) a.cut[blockIdx.x] = ChunkCut{g.nparts, g.row0, g.ntok, g.h};
+      }
+      if (!more) return;
+      // queries: the box is G heads of TB tokens; rows behind the block belong to other
+      // sequences (or none) and their results are not kept
+      if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, a.shape.status)) break;
+      const int ntile = g.split ? 1 : 2;
+      if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, ntile * Y::kHalves * a.TB * a.G * 128);
+      __syncwarp();
+      if (lane < ntile * Y::kHalves) {
+        const int t = lane / Y::kHalves, hf = lane % Y::kHalves;
+        tc::tma_3d(smem + Y::kQ + t * Y::kTileBytes + hf * kHalfBytes, qmap, hf * 64, g.h * a.G,
+                   g.row0 + t * a.TB, &mi.q_full);
+      }
     }
-    if (!more) return;
-    // queries: the box is G heads of TB tokens; rows behind the block belong to other
-    // sequences (or none) and their results are not kept
-    if (n > 0 && !tc::wait_warp(&mi.q_empty, (n - 1) & 1, &mi.quit, a.shape.status)) break;
-    const int ntile = g.split ? 1 : 2;
-    if (lane == 0) mbar_arrive_expect_tx(&mi.q_full, ntile * Y::kHalves * a.TB * a.G * 128);
-    __syncwarp();
-    if (lane < ntile * Y::kHalves) {
-      const int t = lane / Y::kHalves, hf = lane % Y::kHalves;
-      tc::tma_3d(smem + Y::kQ + t * Y::kTileBytes + hf * kHalfBytes, qmap, hf * 64, g.h * a.G,
-                 g.row0 + t * a.TB, &mi.q_full);
-    }
-    if (!load.template tiles<false>(g)) break;
+    if (!load.tiles(g)) break;
     it += 2 * (g.i1 - g.i0);
   }
   load.drain();
-  mbar_wait(&mi.q_full, 0);
-}
-
-template <int D>
-__device__ __forceinline__ void produce_v(const Args& a, uint32_t smem, Misc& mi,
-                                          const CUtensorMap* vmap) {
-  Loader<D> load(a, smem, mi, vmap);
-  for (int n = 0;; ++n) {
-    const int slot = n % kSegs;
-    if (!tc::wait_warp(&mi.seg_full[slot], (n / kSegs) & 1, &mi.quit, a.shape.status)) break;
-    const ChunkSeg g = mi.seg[slot];
-    __syncwarp();
-    if (load.lane == 0) mbar_arrive(&mi.seg_empty[slot]);
-    if (!g.valid) return;
-    if (!load.template tiles<true>(g)) break;
-  }
-  load.drain();
+  if (!values) mbar_wait(&mi.q_full, 0);
 }
 
 // ---- one warp issues every product ----------------------------------------------------
@@ -657,10 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::commit(&mi.drain);
         mbar_wait(&mi.drain, 0);
       }
-    } else if (warp == 9) {
-      produce_k<D>(a, smem, mi, &qmap, &kmap);
-    } else if (warp == 10) {
-      produce_v<D>(a, smem, mi, &vmap);
+    } else if (warp < 11) {
+      produce<D>(a, smem, mi, &qmap, warp == 9 ? &kmap : &vmap, warp == 10);
     }
     __syncwarp();
   }
