@@ -2,7 +2,8 @@
 
 Thin Python binding over the C ABI of ``lib/libsa.so`` (declared in ``include/sa.h``):
 it only marshals torch tensors (device memory) and the current CUDA stream into the
-library's plain pointers and sizes.  Every step of the computation runs in the
+library's plain pointers and sizes (``csrc/binding.cpp`` for the two calls of every step that
+check shapes and types, ctypes elsewhere).  Every step of the computation runs in the
 library's CUDA kernels; there is no Python or CPU fallback, and importing this
 package fails loudly when the library has not been built.
 
@@ -28,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 from typing import Optional
 
@@ -35,6 +37,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libsa.so")
+BINDING_PATH = os.path.join(_HERE, "lib", "_binding.so")
 
 SA_OK = 0
 SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE = -1, -2, -3
@@ -133,7 +136,21 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+def _load_binding(library: ctypes.CDLL):
+    """The compiled argument checks of append_kv and attend_chunk (csrc/binding.cpp)."""
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError("_binding.so is not built (%s); run __graft_entry__.build() or "
+                          "python paged_kv_cache_sa_b200/build.py" % BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+               for f in (library.sa_append_kv, library.sa_attend_chunk)))
+    return mod
+
+
 lib = _load()
+_binding = _load_binding(lib)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -406,71 +423,24 @@ def prune_compact(geom: Geometry, k_cache, v_cache, page_table, seq_lens, keep, 
     return new_page_table, new_seq_lens, pos_map, logical_len
 
 
-_BF16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 values or their bit patterns
-_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
-
-
-def _need(t, name, shape, dtypes, dev):
-    """Address of a dense tensor of this shape and type on CUDA device ``dev`` (ValueError
-    otherwise): the library sees plain pointers and could not tell."""
-    if (t.shape != shape or t.dtype not in dtypes or t.get_device() != dev
-            or not t.is_contiguous()):
-        raise ValueError("%s: need a dense %s of shape %s on cuda:%d, got shape %s strides %s of "
-                         "%s on %s" % (name, dtypes[0], list(shape), dev, list(t.shape),
-                                       list(t.stride()), t.dtype, t.device))
-    return t.data_ptr()
-
-
-def _rows(t, name, heads, width, n, dev):
-    """(address, elements per token) of [n, heads, width] rows; only tokens may be strided."""
-    if t.shape != (n, heads, width) or t.dtype not in _BF16 or t.get_device() != dev:
-        raise ValueError("%s: need shape %s of torch.bfloat16 on cuda:%d, got %s of %s on %s" % (
-            name, [n, heads, width], dev, list(t.shape), t.dtype, t.device))
-    if n == 0:
-        return t.data_ptr() or 16, heads * width
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != width):
-        raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.data_ptr(), s0 if n > 1 else max(s0, heads * width) & ~7
-
-
-def _cuda_index(t) -> int:
-    dev = t.get_device()
+def _call(fn, what, geom, k_cache, ws, stream, *args):
+    """fn(device, geom, *args, workspace, stream) with k_cache's device current, on ``stream`` or
+    the device's own current stream.  The library sees plain pointers and could not tell, so fn
+    checks every tensor's shape, type and device (ValueError)."""
+    dev = k_cache.get_device()
     if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    return dev
-
-
-def _call(fn, what, dev, stream, ws, *args):
-    """fn(*args, workspace, stream) with CUDA device ``dev`` current, on ``stream`` or the
-    device's own current stream."""
-    if ws.buf.get_device() != dev:
-        raise ValueError("the workspace lives on %s, the tensors on cuda:%d" % (ws.buf.device, dev))
-    args += (ws.buf.data_ptr(), ws.nbytes)
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+    buf = ws.buf
+    if buf.get_device() != dev:
+        raise ValueError("the workspace lives on %s, the tensors on cuda:%d" % (buf.device, dev))
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, raw)
+        st = fn(dev, geom, *args, buf.data_ptr(), ws.nbytes, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, raw)
+            st = fn(dev, geom, *args, buf.data_ptr(), ws.nbytes, raw)
     if st != SA_OK:
         raise SaError(st, what)
-
-
-def _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, dev):
-    g = geom
-    cu = _need(cu_new, "cu_new", (g.B + 1,), _I32, dev)
-    pt = _need(page_table, "page_table", (g.B, g.max_pages), _I32, dev)
-    sl = _need(seq_lens, "seq_lens", (g.B,), _I32, dev)
-    kc = _need(k_cache, "k_cache", (g.n_pool, g.Hkv, g.P, g.Dk), _BF16, dev)
-    if g.v_aliases_k:
-        return cu, pt, sl, kc, None
-    if v_cache is None:
-        raise ValueError("v_cache is needed (the geometry's V does not alias K)")
-    return cu, pt, sl, kc, _need(v_cache, "v_cache", (g.n_pool, g.Hkv, g.P, g.Dv), _BF16, dev)
 
 
 def append_kv(geom: Geometry, k, v, cu_new, page_table, seq_lens, k_cache, v_cache,
@@ -485,31 +455,11 @@ def append_kv(geom: Geometry, k, v, cu_new, page_table, seq_lens, k_cache, v_cac
     projection output (only the token stride may differ from dense).  ``inv_freq`` [rot/2]
     fp32 gives the rotated width; None rotates nothing.  Returns ``q_out`` (allocated when
     ``q`` is given without it; rows of no sequence are then undefined), else None."""
-    dev, n = _cuda_index(k_cache), k.shape[0]
-    cu, pt, sl, kc, vc = _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, dev)
-    kp, ks = _rows(k, "k", geom.Hkv, geom.Dk, n, dev)
-    vp = qp = qo = fq = ll = s16 = s8 = None
-    vs = qs = rot = 0
-    if not geom.v_aliases_k:
-        if v is None:
-            raise ValueError("v is needed (the geometry's V does not alias K)")
-        vp, vs = _rows(v, "v", geom.Hkv, geom.Dv, n, dev)
-    if q is not None:
-        qp, qs = _rows(q, "q", geom.Hq, geom.Dk, n, dev)
-        if q_out is None:
-            q_out = torch.empty((n, geom.Hq, geom.Dk), dtype=q.dtype, device=q.device)
-        qo = _need(q_out, "q_out", (n, geom.Hq, geom.Dk), _BF16, dev) if n else qp
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        fq = _need(inv_freq, "inv_freq", (rot // 2,), _F32, dev)
-    if logical_lens is not None:
-        ll = _need(logical_lens, "logical_lens", (geom.B,), _I32, dev)
-    if summ is not None:
-        s16 = _need(summ, "summ", (geom.n_pool, geom.Hkv, 2, geom.Dk), _BF16, dev)
-    if summ8 is not None:
-        s8 = _need(summ8, "summ8", (geom.n_pool, geom.Hkv, 2 * geom.Dk + 16), _U8, dev)
-    _call(lib.sa_append_kv, "sa_append_kv", dev, stream, ws, geom.c(), qp, qs, kp, ks, vp, vs, n, cu,
-          pt, sl, ll, fq, rot_start, rot, 1 if interleaved else 0, qo, kc, vc, s16, s8)
+    if q is not None and q_out is None:
+        q_out = torch.empty((len(k), geom.Hq, geom.Dk), dtype=q.dtype, device=q.device)
+    _call(_binding.append_kv, "sa_append_kv", geom, k_cache, ws, stream, k, v, cu_new, page_table,
+          seq_lens, k_cache, v_cache, q, q_out, inv_freq, rot_start, interleaved, logical_lens,
+          summ, summ8)
     return q_out if q is not None else None
 
 
@@ -519,16 +469,10 @@ def attend_chunk(geom: Geometry, q, cu_new, k_cache, v_cache, page_table, seq_le
     ``cu_new[b]:cu_new[b+1]`` are the last tokens of sequence b) over the paged cache, with
     ``window`` > 0 restricted to ``sink`` first tokens and the last ``window`` ones.  Returns
     (out [n, Hq, Dv] bf16, lse [n, Hq] fp32); rows of no sequence keep what they held."""
-    dev, n = _cuda_index(k_cache), q.shape[0]
-    cu, pt, sl, kc, vc = _batch(geom, cu_new, page_table, seq_lens, k_cache, v_cache, dev)
-    qp = _need(q, "q", (n, geom.Hq, geom.Dk), _BF16, dev)
     if out is None:
-        out = torch.empty((n, geom.Hq, geom.Dv), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((len(q), geom.Hq, geom.Dv), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((n, geom.Hq), dtype=torch.float32, device=q.device)
-    op = _need(out, "out", (n, geom.Hq, geom.Dv), _BF16, dev)
-    lp = _need(lse, "lse", (n, geom.Hq), _F32, dev)
-    if n:
-        _call(lib.sa_attend_chunk, "sa_attend_chunk", dev, stream, ws, geom.c(), qp, n, cu, kc, vc, pt,
-              sl, sink, window, scale, op, lp)
+        lse = torch.empty((len(q), geom.Hq), dtype=torch.float32, device=q.device)
+    _call(_binding.attend_chunk, "sa_attend_chunk", geom, k_cache, ws, stream, q, cu_new, k_cache,
+          v_cache, page_table, seq_lens, sink, window, scale, out, lse)
     return out, lse

@@ -3,7 +3,8 @@
 Each translation unit is compiled in parallel, then linked into one shared library
 that exports only the C ABI declared in ``include/sa.h``.  The CUDA runtime is linked
 statically; the driver's tensor-map encoder is resolved at run time, so the library
-has no link-time dependency on libcuda.
+has no link-time dependency on libcuda.  ``lib/_binding.so`` (csrc/binding.cpp, g++) is the part
+of the Python binding that looks into torch tensors; it links torch and Python, not CUDA.
 """
 
 from __future__ import annotations
@@ -22,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(PKG, "lib", "obj")
 LIB = os.path.join(LIBDIR, "libsa.so")
+BINDING = os.path.join(LIBDIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -77,7 +79,32 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
         os.replace(tmp, lib)
+    if not trace:
+        build_binding(force)
     return lib
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp into lib/_binding.so."""
+    import sysconfig
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    if force or _stale(BINDING, [src, __file__, os.path.join(INCLUDE, "sa.h")]):
+        t = os.path.dirname(torch.__file__)
+        inc = [INCLUDE, os.path.join(t, "include"),
+               os.path.join(t, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include")]
+        tmp = BINDING + ".tmp.%d" % os.getpid()
+        cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
+               + [x for d in inc for x in ("-I", d)]
+               + [src, "-o", tmp, "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu",
+                  "-lc10"])
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
+        os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":
