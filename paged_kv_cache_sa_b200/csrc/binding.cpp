@@ -172,6 +172,7 @@ PyObject* py_append(PyObject*, PyObject* const* x, Py_ssize_t nx) {
     if (x[16] != Py_None)
       s8 = need(x[16], "summ8", {g.n_pool, g.Hkv, 2 * (int64_t)g.Dk + 16}, is_u8, dev);
     const int start = narrow(x[12]), inter = PyObject_IsTrue(x[13]);
+    if (inter < 0) return nullptr;
     void* ws = (void*)integer(x[17]);
     const size_t bytes = (size_t)integer(x[18]);
     void* stream = (void*)integer(x[19]);

@@ -72,6 +72,8 @@ def test_wrong_tensors_are_refused(name):
     if name == "append":
         with pytest.raises(OverflowError):
             run(b, name, good, rot_start=1 << 40)
+        with pytest.raises(RuntimeError):
+            run(b, name, good, interleaved=torch.ones(2))  # no truth value
         with pytest.raises(sa.SaError):
             run(b, name, good, rot_start=4)
     else:
