@@ -415,6 +415,7 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
                          : "memory");
         }
         tc::fence_async_smem();
+        __syncwarp();  // every lane's row is zeroed before this warp hands anything over
       }
       if (any) {
         uint32_t x[128];
