@@ -71,7 +71,7 @@ void* rows(PyObject* o, const char* name, int64_t heads, int64_t width, int64_t 
   if (n == 0) return t.data_ptr() ? t.data_ptr() : reinterpret_cast<void*>(16);
   if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != width))
     refuse(t, name, "the heads of a token side by side", dev);
-  *stride = n > 1 ? t.stride(0) : std::max(t.stride(0), heads * width) & ~int64_t(7);
+  if (n > 1) *stride = t.stride(0);  // (of one row torch keeps whatever stride it was sliced from)
   return t.data_ptr();
 }
 
