@@ -168,6 +168,22 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A buffer that a call on ``stream`` writes and its caller reads on the current stream.  It
+    comes from the pool of ``stream`` (a block of the current stream's may still be used by what
+    is queued there) and, once dropped, is not given out again before the current stream is done
+    with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    reader = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(reader)
+    return t
+
+
 def _check(st: int, what: str):
     if st != SA_OK:
         raise SaError(st, what)
@@ -456,7 +472,7 @@ def append_kv(geom: Geometry, k, v, cu_new, page_table, seq_lens, k_cache, v_cac
     fp32 gives the rotated width; None rotates nothing.  Returns ``q_out`` (allocated when
     ``q`` is given without it; rows of no sequence are then undefined), else None."""
     if q is not None and q_out is None:
-        q_out = torch.empty((len(k), geom.Hq, geom.Dk), dtype=q.dtype, device=q.device)
+        q_out = _empty((len(k), geom.Hq, geom.Dk), q.dtype, q.device, stream)
     _call(_binding.append_kv, "sa_append_kv", geom, k_cache, ws, stream, k, v, cu_new, page_table,
           seq_lens, k_cache, v_cache, q, q_out, inv_freq, rot_start, interleaved, logical_lens,
           summ, summ8)
@@ -470,9 +486,9 @@ def attend_chunk(geom: Geometry, q, cu_new, k_cache, v_cache, page_table, seq_le
     ``window`` > 0 restricted to ``sink`` first tokens and the last ``window`` ones.  Returns
     (out [n, Hq, Dv] bf16, lse [n, Hq] fp32); rows of no sequence keep what they held."""
     if out is None:
-        out = torch.empty((len(q), geom.Hq, geom.Dv), dtype=torch.bfloat16, device=q.device)
+        out = _empty((len(q), geom.Hq, geom.Dv), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((len(q), geom.Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((len(q), geom.Hq), torch.float32, q.device, stream)
     _call(_binding.attend_chunk, "sa_attend_chunk", geom, k_cache, ws, stream, q, cu_new, k_cache,
           v_cache, page_table, seq_lens, sink, window, scale, out, lse)
     return out, lse
