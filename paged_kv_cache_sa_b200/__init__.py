@@ -7,7 +7,8 @@ check shapes and types, ctypes elsewhere).  Every step of the computation runs i
 library's CUDA kernels; there is no Python or CPU fallback, and importing this
 package fails loudly when the library has not been built.
 
-Functions (all asynchronous on ``torch.cuda.current_stream()``):
+Functions (all asynchronous on ``torch.cuda.current_stream()``, or on ``stream=``, from whose
+memory pool outputs that are left out then come):
 
   page_summaries(geom, k_cache, page_table, seq_lens, summ)
   update_summaries(geom, k_cache, page_table, seq_lens, summ, n_tail_pages=1)
@@ -210,7 +211,7 @@ class Workspace:
     def __init__(self, nbytes: int, device=None, stream=None):
         if nbytes <= 0:
             raise ValueError("workspace size must be positive (invalid geometry?)")
-        self.buf = torch.empty(int(nbytes), dtype=torch.uint8, device=device or "cuda")
+        self.buf = _empty(int(nbytes), torch.uint8, device or "cuda", stream)
         self.nbytes = int(nbytes)
         _check(lib.sa_workspace_init(_ptr(self.buf), self.nbytes, _stream(stream)),
                "sa_workspace_init")
@@ -253,8 +254,7 @@ def page_scores(geom: Geometry, q, summ, page_table, seq_lens, ws: Workspace, sc
                 stream=None):
     """Page scores alone: [B][Hkv][max_pages] fp32 (-inf past each sequence's pages)."""
     if scores is None:
-        scores = torch.empty((geom.B, geom.Hkv, geom.max_pages), dtype=torch.float32,
-                             device=q.device)
+        scores = _empty((geom.B, geom.Hkv, geom.max_pages), torch.float32, q.device, stream)
     g = geom.c()
     _check(lib.sa_page_scores(ctypes.byref(g), _ptr(q), _ptr(summ), _ptr(page_table),
                               _ptr(seq_lens), _ptr(scores), _ptr(ws.buf), ws.nbytes,
@@ -271,9 +271,9 @@ def select_pages(geom: Geometry, q, summ, page_table, seq_lens, budget, sink, wi
     K = budget // geom.P
     dev = q.device
     if sel is None:
-        sel = torch.empty((geom.B, geom.Hkv, K), dtype=torch.int32, device=dev)
+        sel = _empty((geom.B, geom.Hkv, K), torch.int32, dev, stream)
     if sel_count is None:
-        sel_count = torch.empty((geom.B, geom.Hkv), dtype=torch.int32, device=dev)
+        sel_count = _empty((geom.B, geom.Hkv), torch.int32, dev, stream)
     g = geom.c()
     _check(lib.sa_select_pages(ctypes.byref(g), _ptr(q), _ptr(summ), _ptr(page_table),
                                _ptr(seq_lens), int(budget), int(sink), int(window),
@@ -289,9 +289,9 @@ def sparse_decode(geom: Geometry, q, k_cache, v_cache, summ, page_table, seq_len
                   sel_count_out=None, n_tail_refresh: int = 0, stream=None):
     dev = q.device
     if out is None:
-        out = torch.empty((geom.B, geom.Hq, geom.Dv), dtype=torch.float32, device=dev)
+        out = _empty((geom.B, geom.Hq, geom.Dv), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((geom.B, geom.Hq), dtype=torch.float32, device=dev)
+        lse = _empty((geom.B, geom.Hq), torch.float32, dev, stream)
     g = geom.c()
     _check(lib.sa_sparse_decode(ctypes.byref(g), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(summ),
                                 _ptr(page_table), _ptr(seq_lens), int(budget), int(sink),
@@ -307,9 +307,9 @@ def sparse_decode_fused(geom: Geometry, q, k_cache, v_cache, summ, page_table, s
     """sparse_decode in one persistent launch (grouped-query geometry)."""
     dev = q.device
     if out is None:
-        out = torch.empty((geom.B, geom.Hq, geom.Dv), dtype=torch.float32, device=dev)
+        out = _empty((geom.B, geom.Hq, geom.Dv), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((geom.B, geom.Hq), dtype=torch.float32, device=dev)
+        lse = _empty((geom.B, geom.Hq), torch.float32, dev, stream)
     g = geom.c()
     _check(lib.sa_sparse_decode_fused(ctypes.byref(g), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                       _ptr(summ), _ptr(page_table), _ptr(seq_lens), int(budget),
@@ -353,8 +353,7 @@ def update_summaries_fp8(geom: Geometry, k_cache, page_table, seq_lens, summ8,
 def page_scores_fp8(geom: Geometry, q, summ8, page_table, seq_lens, ws: Workspace, scores=None,
                     stream=None):
     if scores is None:
-        scores = torch.empty((geom.B, geom.Hkv, geom.max_pages), dtype=torch.float32,
-                             device=q.device)
+        scores = _empty((geom.B, geom.Hkv, geom.max_pages), torch.float32, q.device, stream)
     g = geom.c()
     _check(lib.sa_page_scores_fp8(ctypes.byref(g), _ptr(q), _ptr(summ8), _ptr(page_table),
                                   _ptr(seq_lens), _ptr(scores), _ptr(ws.buf), ws.nbytes,
@@ -367,9 +366,9 @@ def sparse_decode_fp8(geom: Geometry, q, k_cache, v_cache, summ8, page_table, se
                       sel_count_out=None, n_tail_refresh: int = 0, stream=None):
     dev = q.device
     if out is None:
-        out = torch.empty((geom.B, geom.Hq, geom.Dv), dtype=torch.float32, device=dev)
+        out = _empty((geom.B, geom.Hq, geom.Dv), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((geom.B, geom.Hq), dtype=torch.float32, device=dev)
+        lse = _empty((geom.B, geom.Hq), torch.float32, dev, stream)
     g = geom.c()
     _check(lib.sa_sparse_decode_fp8(ctypes.byref(g), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                     _ptr(summ8), _ptr(page_table), _ptr(seq_lens), int(budget),
@@ -387,9 +386,9 @@ def sparse_decode_noalloc(geom: Geometry, q, k_cache, v_cache, summ, page_table,
     """sa_sparse_decode on the library's static scratch (no workspace argument)."""
     dev = q.device
     if out is None:
-        out = torch.empty((geom.B, geom.Hq, geom.Dv), dtype=torch.float32, device=dev)
+        out = _empty((geom.B, geom.Hq, geom.Dv), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((geom.B, geom.Hq), dtype=torch.float32, device=dev)
+        lse = _empty((geom.B, geom.Hq), torch.float32, dev, stream)
     g = geom.c()
     _check(lib.sa_sparse_decode_noalloc(ctypes.byref(g), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                         _ptr(summ), _ptr(page_table), _ptr(seq_lens), int(budget),
@@ -404,9 +403,9 @@ def attend_selected(geom: Geometry, q, k_cache, v_cache, page_table, seq_lens, s
                     scale, ws: Workspace, out=None, lse=None, sel_phys=None, stream=None):
     dev = q.device
     if out is None:
-        out = torch.empty((geom.B, geom.Hq, geom.Dv), dtype=torch.float32, device=dev)
+        out = _empty((geom.B, geom.Hq, geom.Dv), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((geom.B, geom.Hq), dtype=torch.float32, device=dev)
+        lse = _empty((geom.B, geom.Hq), torch.float32, dev, stream)
     g = geom.c()
     _check(lib.sa_attend_selected(ctypes.byref(g), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(page_table), _ptr(seq_lens), _ptr(sel), _ptr(sel_count),
@@ -422,13 +421,13 @@ def prune_compact(geom: Geometry, k_cache, v_cache, page_table, seq_lens, keep, 
     dev = k_cache.device
     width = geom.max_pages * geom.P
     if new_page_table is None:
-        new_page_table = torch.empty((geom.B, geom.max_pages), dtype=torch.int32, device=dev)
+        new_page_table = _empty((geom.B, geom.max_pages), torch.int32, dev, stream)
     if new_seq_lens is None:
-        new_seq_lens = torch.empty((geom.B,), dtype=torch.int32, device=dev)
+        new_seq_lens = _empty((geom.B,), torch.int32, dev, stream)
     if pos_map is None:
-        pos_map = torch.empty((geom.B, width), dtype=torch.int32, device=dev)
+        pos_map = _empty((geom.B, width), torch.int32, dev, stream)
     if logical_len is None:
-        logical_len = torch.empty((geom.B,), dtype=torch.int32, device=dev)
+        logical_len = _empty((geom.B,), torch.int32, dev, stream)
     g = geom.c()
     _check(lib.sa_prune_compact(ctypes.byref(g), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                                 _ptr(seq_lens), _ptr(keep), _ptr(free_pages),

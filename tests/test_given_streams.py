@@ -86,3 +86,85 @@ def check_streams(call):
 @pytest.mark.parametrize("geom", ["llama", "latent"])
 def test_new_token_calls_on_a_given_stream(geom, name):
     check_streams(new_token_calls(geom)[name])
+
+
+def decode_calls(geom, fp8):
+    b = Batch(geom, [1] * 4, [200, 177, 130, 160], seed=42, sigma=0.5)
+    g = b.g
+    table, seq = b.table.cuda(), b.seq.cuda()
+    k = b.k_cache.nan_to_num(0).cuda()
+    v = None if b.latent else b.v_cache.nan_to_num(0).cuda()
+    q = b.normal(g.B, g.Hq, g.Dk).cuda()
+    budget, sink, window = 2 * g.P, 0, g.P
+    ws = sa.Workspace.for_decode(g, budget)
+    summ = torch.zeros(g.n_pool, g.Hkv, 2, g.Dk, dtype=torch.bfloat16, device="cuda")
+    sa.page_summaries(g, k, table, seq, summ)
+    sel, count = sa.select_pages(g, q, summ, table, seq, budget, sink, window, ws)
+    args = (g, q, k, v, summ, table, seq, budget, sink, window, 0.1)
+    calls = {
+        "page_scores": lambda s: (sa.page_scores(g, q, summ, table, seq, ws, stream=s),),
+        "select_pages": lambda s: sa.select_pages(g, q, summ, table, seq, budget, sink, window, ws,
+                                                  stream=s),
+        "sparse_decode": lambda s: sa.sparse_decode(*args, ws, stream=s),
+        "sparse_decode_noalloc": lambda s: sa.sparse_decode_noalloc(*args, stream=s),
+        "attend_selected": lambda s: sa.attend_selected(g, q, k, v, table, seq, sel, count, 0.1,
+                                                        ws, stream=s),
+    }
+    if not b.latent:
+        calls["sparse_decode_fused"] = lambda s: sa.sparse_decode_fused(*args, ws, stream=s)
+    if fp8:
+        summ8 = sa.empty_summaries_fp8(g)
+        sa.page_summaries_fp8(g, k, table, seq, summ8)
+        calls = {
+            "page_scores_fp8": lambda s: (sa.page_scores_fp8(g, q, summ8, table, seq, ws,
+                                                             stream=s),),
+            "sparse_decode_fp8": lambda s: sa.sparse_decode_fp8(
+                g, q, k, v, summ8, table, seq, budget, sink, window, 0.1, ws, stream=s),
+        }
+    return calls
+
+
+@gpu
+@pytest.mark.parametrize("geom,name", [
+    (geom, name) for geom in ("llama", "latent")
+    for name in ("page_scores", "select_pages", "sparse_decode", "sparse_decode_noalloc",
+                 "attend_selected")] + [("llama", "sparse_decode_fused")])
+def test_decode_calls_on_a_given_stream(geom, name):
+    check_streams(decode_calls(geom, False)[name])
+
+
+@gpu
+@pytest.mark.parametrize("name", ["page_scores_fp8", "sparse_decode_fp8"])
+def test_fp8_calls_on_a_given_stream(name):
+    check_streams(decode_calls("llama", True)[name])
+
+
+@gpu
+def test_prune_on_a_given_stream():
+    b = Batch("llama", [1, 1], [200, 77], seed=43, extra_pages=40)
+    g = b.g
+    table, seq = b.table.cuda(), b.seq.cuda()
+    k, v = b.k_cache.nan_to_num(0).cuda(), b.v_cache.nan_to_num(0).cuda()
+    keep = (torch.rand(g.B, g.max_pages * g.P, generator=b.gen) < 0.5).to(torch.uint8).cuda()
+    used = set(b.table[b.table >= 0].tolist())
+    free = torch.tensor([p for p in range(g.n_pool) if p not in used], dtype=torch.int32).cuda()
+    summ = torch.zeros(g.n_pool, g.Hkv, 2, g.Dk, dtype=torch.bfloat16, device="cuda")
+    ws = sa.Workspace.for_prune(g)
+    check_streams(lambda s: sa.prune_compact(g, k, v, table, seq, keep, free, k, v, summ, ws,
+                                             stream=s))
+    assert ws.status() == sa.SA_OK
+
+
+@gpu
+def test_workspace_of_a_given_stream():
+    """The buffer is zeroed on the stream it is made for."""
+    side = torch.cuda.Stream()
+    busy = torch.full((1 << 16,), 3, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SLEEP)
+    copy = busy.clone()
+    del busy
+    ws = sa.Workspace(1 << 16, stream=side)
+    torch.cuda.synchronize()
+    assert bool((copy == 3).all()) and ws.status(side) == sa.SA_OK
+    assert not bool(ws.buf[:256].any())
