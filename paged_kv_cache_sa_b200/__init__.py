@@ -5,7 +5,8 @@ it only marshals torch tensors (device memory) and the current CUDA stream into 
 library's plain pointers and sizes (``csrc/binding.cpp`` for the two calls of every step that
 check shapes and types, ctypes elsewhere).  Every step of the computation runs in the
 library's CUDA kernels; there is no Python or CPU fallback, and importing this
-package fails loudly when the library has not been built.
+package fails loudly when the library has not been built (as do the two calls when their
+compiled part has not).
 
 Functions (all asynchronous on ``torch.cuda.current_stream()``, or on ``stream=``, from whose
 memory pool outputs that are left out then come):
@@ -151,7 +152,15 @@ def _load_binding(library: ctypes.CDLL):
 
 
 lib = _load()
-_binding = _load_binding(lib)
+_binding = None
+
+
+def _compiled():
+    """The compiled part, loaded by the first call that needs it."""
+    global _binding
+    if _binding is None:
+        _binding = _load_binding(lib)
+    return _binding
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -472,7 +481,7 @@ def append_kv(geom: Geometry, k, v, cu_new, page_table, seq_lens, k_cache, v_cac
     ``q`` is given without it; rows of no sequence are then undefined), else None."""
     if q is not None and q_out is None:
         q_out = _empty((len(k), geom.Hq, geom.Dk), q.dtype, q.device, stream)
-    _call(_binding.append_kv, "sa_append_kv", geom, k_cache, ws, stream, k, v, cu_new, page_table,
+    _call(_compiled().append_kv, "sa_append_kv", geom, k_cache, ws, stream, k, v, cu_new, page_table,
           seq_lens, k_cache, v_cache, q, q_out, inv_freq, rot_start, interleaved, logical_lens,
           summ, summ8)
     return q_out if q is not None else None
@@ -488,6 +497,6 @@ def attend_chunk(geom: Geometry, q, cu_new, k_cache, v_cache, page_table, seq_le
         out = _empty((len(q), geom.Hq, geom.Dv), torch.bfloat16, q.device, stream)
     if lse is None:
         lse = _empty((len(q), geom.Hq), torch.float32, q.device, stream)
-    _call(_binding.attend_chunk, "sa_attend_chunk", geom, k_cache, ws, stream, q, cu_new, k_cache,
+    _call(_compiled().attend_chunk, "sa_attend_chunk", geom, k_cache, ws, stream, q, cu_new, k_cache,
           v_cache, page_table, seq_lens, sink, window, scale, out, lse)
     return out, lse
