@@ -33,13 +33,13 @@ import ctypes
 import dataclasses
 import importlib.util
 import os
+import sys
 from typing import Optional
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libsa.so")
-BINDING_PATH = os.path.join(_HERE, "lib", "_binding.so")
 
 SA_OK = 0
 SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE = -1, -2, -3
@@ -138,12 +138,21 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+def binding_path() -> str:
+    """The compiled part of the binding for this Python and this torch, which it is linked to
+    (build.py writes it there)."""
+    return os.path.join(_HERE, "lib", "_binding.%s.torch-%s.so"
+                        % (sys.implementation.cache_tag, torch.__version__))
+
+
 def _load_binding(library: ctypes.CDLL):
     """The compiled argument checks of append_kv and attend_chunk (csrc/binding.cpp)."""
-    if not os.path.exists(BINDING_PATH):
-        raise ImportError("_binding.so is not built (%s); run __graft_entry__.build() or "
-                          "python paged_kv_cache_sa_b200/build.py" % BINDING_PATH)
-    spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+    path = binding_path()
+    if not os.path.exists(path):
+        raise ImportError("the compiled part of the binding is not built (%s); run "
+                          "__graft_entry__.build() or python paged_kv_cache_sa_b200/build.py"
+                          % path)
+    spec = importlib.util.spec_from_file_location("_binding", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value

@@ -3,8 +3,9 @@
 Each translation unit is compiled in parallel, then linked into one shared library
 that exports only the C ABI declared in ``include/sa.h``.  The CUDA runtime is linked
 statically; the driver's tensor-map encoder is resolved at run time, so the library
-has no link-time dependency on libcuda.  ``lib/_binding.so`` (csrc/binding.cpp, g++) is the part
-of the Python binding that looks into torch tensors; it links torch and Python, not CUDA.
+has no link-time dependency on libcuda.  ``lib/_binding.*.so`` (csrc/binding.cpp, g++) is the part
+of the Python binding that looks into torch tensors; it links torch and Python, not CUDA, and
+carries their versions in its name, so that another torch finds no file of the old one.
 """
 
 from __future__ import annotations
@@ -23,7 +24,6 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(PKG, "lib", "obj")
 LIB = os.path.join(LIBDIR, "libsa.so")
-BINDING = os.path.join(LIBDIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -85,16 +85,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), trace: boo
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile csrc/binding.cpp into lib/_binding.so."""
+    """Compile csrc/binding.cpp into lib/_binding.<python>.torch-<version>.so."""
     import sysconfig
     import torch
     src = os.path.join(CSRC, "binding.cpp")
-    if force or _stale(BINDING, [src, __file__, os.path.join(INCLUDE, "sa.h")]):
+    path = os.path.join(LIBDIR, "_binding.%s.torch-%s.so"
+                        % (sys.implementation.cache_tag, torch.__version__))
+    if force or _stale(path, [src, __file__, os.path.join(INCLUDE, "sa.h")]):
         t = os.path.dirname(torch.__file__)
         inc = [INCLUDE, os.path.join(t, "include"),
                os.path.join(t, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_path("include")]
-        tmp = BINDING + ".tmp.%d" % os.getpid()
+        tmp = path + ".tmp.%d" % os.getpid()
         cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                 "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi()]
                + [x for d in inc for x in ("-I", d)]
@@ -103,8 +105,8 @@ def build_binding(force: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
-        os.replace(tmp, BINDING)
-    return BINDING
+        os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

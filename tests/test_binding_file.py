@@ -39,3 +39,34 @@ for call in (lambda: sa.append_kv(g, x, x, x, x, x, x, x, None),
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_another_torch_is_another_file(monkeypatch):
+    """The compiled part is linked to one torch and one Python: under another version it is built
+    anew, however recent the file of the old one, and the old one is not loaded."""
+    spec = importlib.util.spec_from_file_location("_sa_build", os.path.join(PKG, "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    b.build_binding()  # up to date
+    made = []
+
+    def compiler(cmd, **kw):
+        made.append(cmd[cmd.index("-o") + 1])
+        open(made[-1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+    with monkeypatch.context() as m:
+        m.setattr(b.subprocess, "run", compiler)
+        assert os.path.exists(b.build_binding()) and not made
+        m.setattr(torch, "__version__", "0.0.other")
+        path = b.build_binding()
+        try:
+            assert len(made) == 1 and os.path.getsize(path) == 0
+        finally:
+            if made:
+                os.remove(path)
+    import paged_kv_cache_sa_b200 as sa
+    assert os.path.samefile(sa.binding_path(), b.build_binding())
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.other")
+        with pytest.raises(ImportError, match="is not built"):
+            sa._load_binding(sa.lib)
