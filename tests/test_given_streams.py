@@ -168,3 +168,26 @@ def test_workspace_of_a_given_stream():
     torch.cuda.synchronize()
     assert bool((copy == 3).all()) and ws.status(side) == sa.SA_OK
     assert not bool(ws.buf[:256].any())
+
+
+@gpu
+@pytest.mark.parametrize("geom", ["llama", "latent"])
+def test_a_given_stream_inside_a_capture(geom):
+    """A captured step whose calls run on a second stream: the outputs are the graph's."""
+    calls = new_token_calls(geom)
+    want = calls["append_kv"](None) + calls["attend_chunk"](None)
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        got = calls["append_kv"](side) + calls["attend_chunk"](side)
+        main.wait_stream(side)
+        copies = [x.clone() for x in got]
+    for _ in range(3):
+        for x in got + tuple(copies):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, c, w in zip(got, copies, want):
+            assert torch.equal(bits(x), bits(w)) and torch.equal(bits(c), bits(w))
