@@ -415,7 +415,6 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
                          : "memory");
         }
         tc::fence_async_smem();
-        __syncwarp();  // every lane's row is zeroed before this warp hands anything over
       }
       if (any) {
         uint32_t x[128];
@@ -491,8 +490,9 @@ __device__ __forceinline__ void soften(const Args& a, uint32_t smem, Misc& mi, u
         tc::unpair(sum[1], a2, a3);
         l += (a0 + a1) + (a2 + a3);
         tc::tmem_wait_st();
-      } else if (lane == 0) {
-        mbar_arrive(&mi.p_part[t]);
+      } else {
+        __syncwarp();  // every lane's row of V is zeroed before this warp hands the tile over
+        if (lane == 0) mbar_arrive(&mi.p_part[t]);
       }
       tc::fence_before();
       __syncwarp();
