@@ -375,15 +375,17 @@ int sa_append_kv(const sa_geom* g, const void* q, int64_t q_stride, const void* 
  *   x_t = scale * q . k_t;  out = sum_t softmax(x)_t v_t;  lse = log sum_t exp(x_t).
  *   q [n_tokens][Hq][Dk] bf16, out [n_tokens][Hq][Dv] bf16 (the operand of the output
  *   projection; half the bytes of the decode calls' fp32), lse [n_tokens][Hq] fp32.
- * scale: positive, at most 2e38 (the softmax works in base 2).  Scores, softmax statistics and sums are fp32; the
- * probabilities are rounded to bf16 (relative to a running maximum) for the product with V,
- * and out once at the end.  Storage behind seq_lens[b] is never used, and neither are pages
+ * scale: positive, at most 2e38 (the softmax works in base 2).  Scores, softmax statistics and
+ * sums are fp32: a row with some |x_t| above 2.3e38 is unspecified.  The probabilities are
+ * rounded to bf16 (relative to a running maximum) for the product with V, and out once at the
+ * end.  Storage behind seq_lens[b] is never used, and neither are pages
  * all of whose tokens a window hides (their table entries may be anything).  The same call
  * repeats bit for bit; a row's last bits depend on how the batch divides the work.  A
  * page-table entry outside [0, n_pool) of a page holding visible tokens is reported as
  * SA_ERR_DEVICE_CHECK; the rows of that sequence are then unspecified.  Whether a page that
  * only holds later tokens of the sequence than a row may see is read for that row is not
- * specified (its tokens are valid and finite by the precondition above).  One new token per sequence (n_b = 1) is the dense decode.
+ * specified (its tokens are valid and finite by the precondition above).  One new token per
+ * sequence (n_b = 1) is the dense decode.
  * sa_chunk_workspace_size: bytes needed for up to n_tokens rows (0 on invalid arguments);
  * any decode workspace of at least that size serves too. */
 size_t sa_chunk_workspace_size(const sa_geom* g, int n_tokens);

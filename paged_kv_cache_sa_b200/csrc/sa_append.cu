@@ -30,11 +30,11 @@
 // walks the rows, so that loads and stores stay 16 bytes wide and coalesced and little is spent
 // on addresses (a count through all units of a run instead: 76 us for the 16390 tokens).
 // Bound by HBM: every row is read once and written once.
-// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 70.5 us (5.8 TB/s; the copy
-// reaches 6.5), 961 tokens of the latent geometry 50.3 us (5.7 TB/s), eight decode tokens 5 us
-// (latency: lengths, page table, keys and sine table one behind the other).  Runs of 2048 units
-// are 6% slower and of 512 13%, 128 threads a CTA 5% faster here but 25% slower for a decode
-// step.  Latent pieces of 30 KB, four stages or fewer and larger CTAs: 1 to 7% slower.
+// Measured on a B200: 16390 tokens of 32 / 8 heads of 128 channels 69.3 us in a graph on one input,
+// 72.6 on changing ones (5.9 and 5.6 TB/s; the copy reaches 6.5), 961 tokens of the latent geometry
+// 50 us (5.7 TB/s), eight decode tokens 4.5 us (latency: lengths, page table, keys and sine table
+// one behind the other).  Runs of 2048 units are 6% slower and of 512 13%, 128 threads a CTA 5%
+// faster here but 25% slower for a decode step.  Latent pieces of 30 KB, four stages or fewer and larger CTAs: 1 to 7% slower.
 #include <algorithm>
 
 #include "sa_common.cuh"

@@ -17,7 +17,8 @@
 //   padding cost tensor time (1024 cycles per 64 KB key tile), which HBM hides (2800 cycles).
 // Per tile: S = Q K^T (128 x 128 x Dk) from shared memory; four softmax warps (thread = row)
 // read S, subtract the row's maximum, write P in bf16 over S's columns and O += P V
-// (128 x Dv x 128) takes P from tensor memory.  While one chain's softmax runs, the other
+// (128 x Dv x 128) takes P from tensor memory.  (bf16 because V is and a product's operands have
+// one type: half a step, 2^-9 to 2^-8, of each probability.  l sums them before that rounding.)  While one chain's softmax runs, the other
 // chain's two products do.
 // The maximum in use is only raised when a row's new maximum exceeds it by more than 2^8
 // (P then stays below 2^8, exact in range for bf16 and fp32): O is rescaled a few times per
@@ -25,10 +26,11 @@
 // Warps 0-3 and 4-7: softmax of chain 0 and 1; 8: issues the products; 9: work list, queries
 // and K; 10: V (one warp for both had the copies of 16-token pages queue behind one another:
 // 212 us instead of 184 for the decode rows below).
-// Measured on a B200, 32 / 8 heads of 128 channels: eight decode rows at 32768 tokens 166 us
-// (6.5 TB/s, HBM), 8192 rows at 32768 2.95 ms (1.3 PFLOP/s, tensor pipe 65% busy: a chain waits
-// for its softmax, some 2000 cycles a tile, and for its own products between two tiles; four
-// products of a step take 2048).  Pieces of few tiles pay about two tiles for starting and ending.
+// Measured on a B200, 32 / 8 heads of 128 channels, in short graphs at up to 1965 MHz: eight decode
+// rows at 32768 tokens 165 us (6.5 TB/s, HBM), 8192 rows at 32768 2.95 ms (1.3 PFLOP/s, tensor pipe
+// 65% busy: a chain waits for its softmax, some 2000 cycles a tile, and for its own products between
+// two tiles; four products of a step take 2048).  At sustained clocks, on changing inputs: 178 us and
+// 3.35 ms.  Pieces of few tiles pay about two tiles for starting and ending.
 #include "sa_chunk.cuh"
 #include "sa_internal.h"
 #include "sa_tc.cuh"

@@ -13,7 +13,8 @@
 // another), kept in workspace slots 2 c and 2 c + 1 of CTA c and joined by a second kernel.
 // When there is at least four times as much to do per CTA as the longest item takes, nothing is
 // cut: whole items, the longest blocks of a head first, go to the CTAs in rounds, forwards and
-// backwards in turn.  That keeps the CTAs on the same head and so on the same keys in L2.  (A
+// backwards in turn.  That keeps the CTAs on the same head and so on the same keys in L2; where the
+// last round holds few items, the fullest CTA has up to 1.24 times the mean.  (A
 // counter to draw from, in place of the rounds, is 1-4% faster on long chunks and up to 2%
 // slower on short ones, and would have to be zero before every call.)
 // With inner > 1 the head groups of one piece go to `inner` neighbouring CTAs at the same time

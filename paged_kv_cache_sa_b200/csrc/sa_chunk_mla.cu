@@ -20,9 +20,11 @@
 // finds); sums stay in the threads until the end.
 // Warps 0-3 and 4-7: softmax; 8: issues the products (even CTA); 9: work list, queries and
 // keys; 10: values.
-// Measured on a B200: 256 + 100 rows at 16384 / 5001 tokens 0.90 ms (1.4 PFLOP/s, tensor pipe 78%
-// busy); sixteen decode rows at 16384 80 us (tensor pipe 49%, DRAM 52%: about 3000 cycles a tile
-// against 2176 for its products, the first tile's 32 MB for all CTAs and the joining).
+// Probabilities are bf16 in the second product, as there.
+// Measured on a B200 in short graphs at up to 1965 MHz: 256 + 100 rows at 16384 / 5001 tokens 0.90 ms
+// (1.4 PFLOP/s, tensor pipe 78% busy); sixteen decode rows at 16384 80 us (tensor pipe 49%, DRAM
+// 52%: about 3000 cycles a tile against 2176 for its products, the first tile's 32 MB for all CTAs
+// and the joining).  At sustained clocks, on changing inputs: 1.05 ms and 94 us.
 #include "sa_chunk.cuh"
 #include "sa_internal.h"
 #include "sa_tc.cuh"
