@@ -191,3 +191,20 @@ def test_a_given_stream_inside_a_capture(geom):
         torch.cuda.synchronize()
         for x, c, w in zip(got, copies, want):
             assert torch.equal(bits(x), bits(w)) and torch.equal(bits(c), bits(w))
+
+
+@gpu
+def test_any_object_with_a_stream_handle():
+    """A stream of another library: only its handle is looked at."""
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+    calls = dict(new_token_calls("llama"), **decode_calls("llama", False))
+    for name in ("append_kv", "attend_chunk", "sparse_decode"):
+        want = calls[name](None)
+        torch.cuda.synchronize()
+        got = calls[name](Handle)
+        torch.cuda.synchronize()
+        for x, w in zip(got, want):
+            assert torch.equal(bits(x), bits(w))
