@@ -231,8 +231,9 @@ class Workspace:
             raise ValueError("workspace size must be positive (invalid geometry?)")
         self.buf = _empty(int(nbytes), torch.uint8, device or "cuda", stream)
         self.nbytes = int(nbytes)
-        _check(lib.sa_workspace_init(_ptr(self.buf), self.nbytes, _stream(stream)),
-               "sa_workspace_init")
+        with torch.cuda.device(self.buf.device):
+            _check(lib.sa_workspace_init(_ptr(self.buf), self.nbytes, _stream(stream)),
+                   "sa_workspace_init")
 
     @classmethod
     def for_decode(cls, geom: Geometry, budget: int, **kw) -> "Workspace":
@@ -248,8 +249,10 @@ class Workspace:
         return cls(prune_workspace_size(geom), **kw)
 
     def status(self, stream=None) -> int:
-        """Synchronise the stream and return (and clear) the device status word."""
-        return int(lib.sa_workspace_status(_ptr(self.buf), _stream(stream)))
+        """Synchronise the stream (the workspace's device's current one) and return (and clear)
+        the device status word."""
+        with torch.cuda.device(self.buf.device):
+            return int(lib.sa_workspace_status(_ptr(self.buf), _stream(stream)))
 
 
 def page_summaries(geom: Geometry, k_cache, page_table, seq_lens, summ, stream=None):
