@@ -18,8 +18,8 @@
 // Per tile: S = Q K^T (128 x 128 x Dk) from shared memory; four softmax warps (thread = row)
 // read S, subtract the row's maximum, write P in bf16 over S's columns and O += P V
 // (128 x Dv x 128) takes P from tensor memory.  (bf16 because V is and a product's operands have
-// one type: half a step, 2^-9 to 2^-8, of each probability.  l sums them before that rounding.)  While one chain's softmax runs, the other
-// chain's two products do.
+// one type: half a step, 2^-9 to 2^-8, of each probability; l sums them before that rounding.)
+// While one chain's softmax runs, the other chain's two products do.
 // The maximum in use is only raised when a row's new maximum exceeds it by more than 2^8
 // (P then stays below 2^8, exact in range for bf16 and fp32): O is rescaled a few times per
 // row instead of at every tile, by the softmax warps themselves.
